@@ -11,16 +11,18 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "tlc.hip")
+SOURCES = [SRC, os.path.join(PKG, "csrc", "ckpt8.hip"), os.path.join(PKG, "csrc", "ckpt8_matrix.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libtlc.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-fno-gpu-flush-denormals-to-zero", "-ffp-contract=off",
     "-Wall", "-Werror=return-type",
@@ -34,19 +36,33 @@ def hipcc() -> str:
     return "hipcc"
 
 
-def command(out: str = LIB) -> list[str]:
-    return [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, SRC, "-o", out]
+def compile_command(src: str, out: str) -> list[str]:
+    return [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-c", src, "-o", out]
+
+
+def link_command(objects: list[str], out: str) -> list[str]:
+    return [hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", out]
 
 
 def build(out: str = LIB, quiet: bool = True) -> str:
+    """Compile the sources side by side and link them."""
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + ".tmp"
-    r = subprocess.run(command(tmp), capture_output=True, text=True)
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, os.path.basename(s) + ".o") for s in SOURCES]
+        runs = [subprocess.Popen(compile_command(s, o), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+                for s, o in zip(SOURCES, objects)]
+        said = [r.communicate()[0] for r in runs]
+        for src, r, text in zip(SOURCES, runs, said):
+            if r.returncode != 0:
+                sys.stderr.write(text)
+                raise RuntimeError(f"hipcc failed ({r.returncode}) building {os.path.basename(src)}")
+            if not quiet:
+                sys.stderr.write(text)
+        r = subprocess.run(link_command(objects, tmp), capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed ({r.returncode}) building {out}")
-    if not quiet:
-        sys.stderr.write(r.stderr)
+        raise RuntimeError(f"hipcc failed ({r.returncode}) linking {out}")
     os.replace(tmp, out)
     return out
 

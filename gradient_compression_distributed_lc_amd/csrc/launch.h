@@ -1,0 +1,50 @@
+// launch.h -- kernel launches of the library: one place that reports a failed
+// launch and, while profiling is on, brackets the kernel with events.
+#ifndef TLC_LAUNCH_H
+#define TLC_LAUNCH_H
+
+#include <hip/hip_runtime.h>
+
+#include <string.h>
+
+#include <mutex>
+#include <vector>
+
+#include "tlc.h"
+
+namespace tlc_internal {
+
+struct ProfRec {
+    const char* name;
+    hipEvent_t a, b;
+};
+inline std::mutex g_prof_mu;
+inline bool g_prof_on = false;
+inline char g_prof_only[48] = {0};  // when set, only this kernel is bracketed
+inline std::vector<ProfRec> g_prof;
+
+template <typename Launch>
+int launch(const char* name, hipStream_t st, Launch&& fn) {
+    hipEvent_t a = nullptr, b = nullptr;
+    bool prof;
+    {
+        std::lock_guard<std::mutex> lk(g_prof_mu);
+        prof = g_prof_on && (!g_prof_only[0] || strcmp(g_prof_only, name) == 0);
+    }
+    if (prof) {
+        if (hipEventCreate(&a) != hipSuccess || hipEventCreate(&b) != hipSuccess) return TLC_ERR_HIP;
+        if (hipEventRecord(a, st) != hipSuccess) return TLC_ERR_HIP;
+    }
+    fn();
+    if (hipGetLastError() != hipSuccess) return TLC_ERR_HIP;
+    if (prof) {
+        if (hipEventRecord(b, st) != hipSuccess) return TLC_ERR_HIP;
+        std::lock_guard<std::mutex> lk(g_prof_mu);
+        g_prof.push_back({name, a, b});
+    }
+    return TLC_OK;
+}
+
+}  // namespace tlc_internal
+
+#endif  // TLC_LAUNCH_H

@@ -75,6 +75,7 @@
 #include <mutex>
 #include <vector>
 
+#include "launch.h"
 #include "tlc.h"
 
 namespace {
@@ -2804,36 +2805,12 @@ __global__ __launch_bounds__(kThreads) void k_wire_copy(GroupView g, const uint8
 // ---------------------------------------------------------------------------
 // host side
 
-struct ProfRec {
-    const char* name;
-    hipEvent_t a, b;
-};
-std::mutex g_prof_mu;
-bool g_prof_on = false;
-char g_prof_only[48] = {0};  // when set, only this kernel is bracketed
-std::vector<ProfRec> g_prof;
-
-template <typename Launch>
-int launch(const char* name, hipStream_t st, Launch&& fn) {
-    hipEvent_t a = nullptr, b = nullptr;
-    bool prof;
-    {
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        prof = g_prof_on && (!g_prof_only[0] || strcmp(g_prof_only, name) == 0);
-    }
-    if (prof) {
-        if (hipEventCreate(&a) != hipSuccess || hipEventCreate(&b) != hipSuccess) return TLC_ERR_HIP;
-        if (hipEventRecord(a, st) != hipSuccess) return TLC_ERR_HIP;
-    }
-    fn();
-    if (hipGetLastError() != hipSuccess) return TLC_ERR_HIP;
-    if (prof) {
-        if (hipEventRecord(b, st) != hipSuccess) return TLC_ERR_HIP;
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        g_prof.push_back({name, a, b});
-    }
-    return TLC_OK;
-}
+using tlc_internal::g_prof;
+using tlc_internal::g_prof_mu;
+using tlc_internal::g_prof_on;
+using tlc_internal::g_prof_only;
+using tlc_internal::launch;
+using tlc_internal::ProfRec;
 
 // Blocks of a grid-looping kernel that are resident on the current device at
 // once (occupancy per CU times the CU count, at most `cap`), queried once per

@@ -90,6 +90,19 @@ _SIGS = {
     "tlc_planes_scatter": (_I, [_P, _P, _P, _P, _P, _U32, _U64, _P]),
     "tlc_gather_probe": (_I, [_P, _P, _U64, _P, _P]),
     "tlc_copy_probe": (_I, [_P, _P, _U64, _P]),
+    "tlc_ckpt8_code_stride": (_U64, [_U64]),
+    "tlc_ckpt8_scale_stride": (_U64, [_U64]),
+    "tlc_ckpt8_pack": (_I, [_P, _U64, _I, _U64, _U64, _I, _P, _P, _P]),
+    "tlc_ckpt8_unpack": (_I, [_P, _P, _I, _U64, _U64, _P, _U64, _I, _P]),
+    "tlc_ckpt8_act": (_I, [_I, _P, _U64, _P, _U64, _I, _U64, _U64, _P, _U64, _I, _P, _P, _P, _P, _P]),
+    "tlc_ckpt8_act_grad": (_I, [_I, _P, _P, _P, _P, _I, _P, _U64, _I, _U64, _U64, _P, _U64, _P, _U64, _P, _P, _P]),
+    "tlc_ckpt8_norm": (_I, [_P, _U64, _P, _U64, _I, _U64, _U64, _P, _I, _F, _I, _P, _U64, _P, _U64, _I, _P, _P, _P,
+                            _P]),
+    "tlc_ckpt8_norm_grad_workspace_size": (_SZ, [_U64, _U64]),
+    "tlc_ckpt8_norm_grad": (_I, [_P, _U64, _P, _U64, _I, _U64, _U64, _P, _U64, _I, _P, _P, _P, _P, _I, _P, _U64, _P,
+                                 _I, _P, _SZ, _P]),
+    "tlc_ckpt8_weight_grad_workspace_size": (_SZ, [_U64, _U64, _U64]),
+    "tlc_ckpt8_weight_grad": (_I, [_P, _U64, _I, _U64, _U64, _I, _P, _P, _U64, _P, _I, _P, _U64, _I, _P, _SZ, _P]),
     "tlc_profile_enable": (_I, [_I]),
     "tlc_profile_read": (_I, [ctypes.POINTER(KernelTime), _I, ctypes.POINTER(_I)]),
     "tlc_profile_only": (_I, [ctypes.c_char_p]),
@@ -734,6 +747,341 @@ def planes_scatter(src: torch.Tensor, src_off: torch.Tensor, dst: torch.Tensor, 
                                     _ptr(dst, torch.float32, "dst"), _ptr(dst_off, torch.int64, "dst_off"),
                                     _ptr(n, torch.int64, "n"), n.numel(), int(max_n), _stream(stream)),
            "tlc_planes_scatter")
+
+
+# ---- 8-bit checkpoints of activations ----------------------------------------
+#
+# Matrices are 2-D tensors with adjacent columns (rows may lie further apart,
+# so halves of a fused projection need no copy).  The calls run on the device
+# of their tensors and on `stream`, or that device's current stream; buffers
+# that are not passed are allocated there, for that stream.
+
+CKPT8_INT8 = 1  # two's complement codes, -127..127
+CKPT8_E4M3 = 2  # 8-bit floats of 4 exponent and 3 fraction bits
+ACT_GELU = 1
+ACT_GELU_TANH = 2
+ACT_SILU = 3
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+@dataclass
+class Checkpoint8:
+    """A matrix [rows, cols] kept in 8 bits: a code per value and a power-of-two
+    scale per 32 columns of a row (layout in tlc.h).  Rows can be sliced off as
+    ``Checkpoint8(c.codes[a:b], c.scales[a:b], c.cols, c.format)``."""
+    codes: torch.Tensor   # uint8[rows, 32*ceil(cols/32)]
+    scales: torch.Tensor  # uint8[rows, 4*ceil(cols/128)]
+    cols: int
+    format: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def ckpt8_code_stride(cols: int) -> int:
+    return int(lib().tlc_ckpt8_code_stride(cols))
+
+
+def ckpt8_scale_stride(cols: int) -> int:
+    return int(lib().tlc_ckpt8_scale_stride(cols))
+
+
+def _matrix(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """(pointer, row stride) of a matrix; with `like`, one of its shape, dtype and device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a matrix with at least one column, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    row, col = t.stride()
+    if col != 1 and cols != 1 or row < cols and rows > 1:
+        raise ValueError(f"{name} must have adjacent columns and rows that do not overlap, got strides {t.stride()}")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr(), row if rows > 1 else cols
+
+
+def _vector(t: torch.Tensor | None, n: int, device, name: str, dtype: torch.dtype | None = None):
+    """(pointer, dtype code) of a vector of n values, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in _DTYPES or dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} values, got shape {tuple(t.shape)}")
+    return t.data_ptr(), _DTYPES[t.dtype]
+
+
+def _format(fmt: int):
+    if fmt != CKPT8_INT8 and fmt != CKPT8_E4M3:
+        raise ValueError(f"unknown checkpoint format {fmt!r}")
+
+
+def _checkpoint(c: Checkpoint8, name: str, rows: int, cols: int, device):
+    """(codes pointer, scales pointer) of a checkpoint of a matrix [rows, cols]."""
+    _format(c.format)
+    if c.cols != cols:
+        raise ValueError(f"{name} must hold {cols} columns, got {c.cols}")
+    groups = -(-cols // 32)
+    for t, what, width in ((c.codes, "codes", 32 * groups), (c.scales, "scales", -(-groups // 4) * 4)):
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name}.{what} must be on {device}, got {t.device}")
+        if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width \
+                or not t.is_contiguous():
+            raise ValueError(f"{name}.{what} must be contiguous uint8[{rows}, {width}], got "
+                             f"{tuple(t.shape)} of {t.dtype}")
+    return c.codes.data_ptr(), c.scales.data_ptr()
+
+
+def _new_checkpoint(rows: int, cols: int, fmt: int, device) -> Checkpoint8:
+    groups = -(-cols // 32)
+    return Checkpoint8(torch.empty((rows, 32 * groups), dtype=torch.uint8, device=device),
+                       torch.empty((rows, -(-groups // 4) * 4), dtype=torch.uint8, device=device), cols, fmt)
+
+
+def _on_stream(device, stream, body):
+    """body(stream handle) with `device` and `stream` (or the device's current one) current."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return body(torch.cuda.current_stream().cuda_stream)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _ckpt8_workspace(nbytes: int, device, workspace):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or workspace.dtype != torch.uint8 \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous uint8 on {device}")
+    return workspace
+
+
+def ckpt8_pack(x: torch.Tensor, fmt: int, *, out: Checkpoint8 | None = None, stream=None) -> Checkpoint8:
+    """The 8-bit checkpoint of a matrix."""
+    px, sx = _matrix(x, "x")
+    _format(fmt)
+    rows, cols = x.shape
+
+    def body(st):
+        c = out if out is not None else _new_checkpoint(rows, cols, fmt, x.device)
+        pc, ps = _checkpoint(c, "out", rows, cols, x.device)
+        if c.format != fmt:
+            raise ValueError("out is of another format")
+        _check(lib().tlc_ckpt8_pack(px, sx, _DTYPES[x.dtype], rows, cols, fmt, pc, ps, st), "tlc_ckpt8_pack")
+        return c
+    return _on_stream(x.device, stream, body)
+
+
+def ckpt8_unpack(c: Checkpoint8, dtype: torch.dtype = torch.bfloat16, *, y: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for (exact in float32 and bfloat16)."""
+    rows, cols, device = c.rows, c.cols, c.codes.device
+    pc, ps = _checkpoint(c, "checkpoint", rows, cols, device)
+
+    def body(st):
+        o = y if y is not None else torch.empty((rows, cols), dtype=dtype, device=device)
+        po, so = _matrix(o, "y")
+        if o.shape[0] != rows or o.shape[1] != cols or o.device != device:
+            raise ValueError(f"y must be ({rows}, {cols}) on {device}")
+        _check(lib().tlc_ckpt8_unpack(pc, ps, c.format, rows, cols, po, so, _DTYPES[o.dtype], st),
+               "tlc_ckpt8_unpack")
+        return o
+    return _on_stream(device, stream, body)
+
+
+def ckpt8_act(a: torch.Tensor, act: int, fmt: int, b: torch.Tensor | None = None, *, y: torch.Tensor | None = None,
+              a_out: Checkpoint8 | None = None, b_out: Checkpoint8 | None = None, stream=None):
+    """y = f(a), or f(a)*b, with the checkpoints of a and b in the same pass.
+    Returns (y, checkpoint of a, checkpoint of b or None)."""
+    pa, sa = _matrix(a, "a")
+    _format(fmt)
+    pb, sb = _matrix(b, "b", a) if b is not None else (None, 0)
+    rows, cols = a.shape
+    device = a.device
+    if b is None and b_out is not None:
+        raise ValueError("b_out needs b")
+
+    def body(st):
+        o = y if y is not None else torch.empty((rows, cols), dtype=a.dtype, device=device)
+        po, so = _matrix(o, "y", a)
+        ca = a_out if a_out is not None else _new_checkpoint(rows, cols, fmt, device)
+        cb = None if b is None else b_out if b_out is not None else _new_checkpoint(rows, cols, fmt, device)
+        pca, psa = _checkpoint(ca, "a_out", rows, cols, device)
+        pcb, psb = _checkpoint(cb, "b_out", rows, cols, device) if cb is not None else (None, None)
+        if ca.format != fmt or cb is not None and cb.format != fmt:
+            raise ValueError("an output checkpoint is of another format")
+        _check(lib().tlc_ckpt8_act(act, pa, sa, pb, sb, _DTYPES[a.dtype], rows, cols, po, so, fmt, pca, psa, pcb,
+                                   psb, st), "tlc_ckpt8_act")
+        return o, ca, cb
+    return _on_stream(device, stream, body)
+
+
+def ckpt8_act_grad(dy: torch.Tensor, act: int, a: Checkpoint8, b: Checkpoint8 | None = None, *,
+                   da: torch.Tensor | None = None, db: torch.Tensor | None = None, want_y: bool = False,
+                   y_out: Checkpoint8 | None = None, stream=None):
+    """Gradient of f(a), or f(a)*b, from the checkpoints.  Returns (da, db or
+    None, the checkpoint of f(a) or f(a)*b if want_y or y_out, else None)."""
+    pd, sd = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    device = dy.device
+    pca, psa = _checkpoint(a, "a", rows, cols, device)
+    pcb, psb = _checkpoint(b, "b", rows, cols, device) if b is not None else (None, None)
+    if b is not None and b.format != a.format:
+        raise ValueError("a and b must be of one format")
+    if b is None and db is not None:
+        raise ValueError("db needs b")
+
+    def body(st):
+        oa = da if da is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
+        poa, soa = _matrix(oa, "da", dy)
+        ob, pob, sob = None, None, 0
+        if b is not None:
+            ob = db if db is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
+            pob, sob = _matrix(ob, "db", dy)
+        cy, pcy, psy = y_out, None, None
+        if cy is None and want_y:
+            cy = _new_checkpoint(rows, cols, a.format, device)
+        if cy is not None:
+            pcy, psy = _checkpoint(cy, "y_out", rows, cols, device)
+            if cy.format != a.format:
+                raise ValueError("y_out is of another format")
+        _check(lib().tlc_ckpt8_act_grad(act, pca, psa, pcb, psb, a.format, pd, sd, _DTYPES[dy.dtype], rows, cols, poa,
+                                        soa, pob, sob, pcy, psy, st), "tlc_ckpt8_act_grad")
+        return oa, ob, cy
+    return _on_stream(device, stream, body)
+
+
+def ckpt8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, fmt: int | None, *,
+               residual: torch.Tensor | None = None, weighted: bool = False, total: torch.Tensor | None = None,
+               y: torch.Tensor | None = None, want_y: bool = True, out: Checkpoint8 | None = None,
+               rstd: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of x + residual.  Returns (sum, y, checkpoint,
+    rstd): sum is x itself without a residual, y is None with want_y False, the
+    checkpoint (of the normalised values, or with `weighted` of them times the
+    weight) is None with fmt None."""
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+    device = x.device
+    pr, sr = _matrix(residual, "residual", x) if residual is not None else (None, 0)
+    pw, wdt = _vector(weight, cols, device, "weight")
+    if fmt is not None:
+        _format(fmt)
+    elif out is not None:
+        raise ValueError("out needs a format")
+    if residual is None and total is not None:
+        raise ValueError("total needs residual: without one the sum is x")
+
+    def body(st):
+        t, pt, stt = x, None, 0
+        if residual is not None:
+            t = total if total is not None else torch.empty((rows, cols), dtype=x.dtype, device=device)
+            pt, stt = _matrix(t, "total", x)
+        o, po, so = y, None, 0
+        if o is None and want_y:
+            o = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        if o is not None:
+            po, so = _matrix(o, "y", x)
+        c, pc, ps = None, None, None
+        if fmt is not None:
+            c = out if out is not None else _new_checkpoint(rows, cols, fmt, device)
+            pc, ps = _checkpoint(c, "out", rows, cols, device)
+            if c.format != fmt:
+                raise ValueError("out is of another format")
+        r = rstd if rstd is not None else torch.empty(rows, dtype=torch.float32, device=device)
+        _check(lib().tlc_ckpt8_norm(px, sx, pr, sr, _DTYPES[x.dtype], rows, cols, pw, wdt, eps, int(weighted), pt, stt,
+                                    po, so, fmt or 0, pc, ps, _vector(r, rows, device, "rstd", torch.float32)[0], st),
+               "tlc_ckpt8_norm")
+        return t, o, c, r
+    return _on_stream(device, stream, body)
+
+
+def ckpt8_norm_grad_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().tlc_ckpt8_norm_grad_workspace_size(rows, cols))
+
+
+def ckpt8_norm_grad(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torch.Tensor | None = None, *,
+                    dtotal: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                    dw: torch.Tensor | None = None, want_dw: bool = True, accumulate: bool = False,
+                    workspace=None, stream=None):
+    """Gradient of the norm.  saved: the checkpoint ckpt8_norm made of the
+    normalised values (not a weighted one), or the sum itself.  dtotal: the
+    gradient that reaches the sum from elsewhere.  Returns (dx, dw or None);
+    dx is the gradient of x and of the residual, dw (float32) is added to with
+    `accumulate`."""
+    pd, sd = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    device = dy.device
+    pc = ps = pt = None
+    stt = fmt = 0
+    if isinstance(saved, Checkpoint8):
+        pc, ps = _checkpoint(saved, "saved", rows, cols, device)
+        fmt = saved.format
+    else:
+        pt, stt = _matrix(saved, "saved", dy)
+    pr, _ = _vector(rstd, rows, device, "rstd", torch.float32)
+    pw, wdt = _vector(weight, cols, device, "weight")
+    pt2, st2 = _matrix(dtotal, "dtotal", dy) if dtotal is not None else (None, 0)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+
+    def body(st):
+        o = dx if dx is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
+        po, so = _matrix(o, "dx", dy)
+        g = dw
+        if g is None and want_dw:
+            g = torch.empty(cols, dtype=torch.float32, device=device)
+        pg, _ = _vector(g, cols, device, "dw", torch.float32)
+        pws, nws = None, 0
+        if g is not None:
+            ws = _ckpt8_workspace(ckpt8_norm_grad_workspace_size(rows, cols), device, workspace)
+            pws, nws = ws.data_ptr(), ws.numel()
+        _check(lib().tlc_ckpt8_norm_grad(pd, sd, pt2, st2, _DTYPES[dy.dtype], rows, cols, pt, stt, fmt, pc, ps, pr,
+                                         pw, wdt, po, so, pg, int(accumulate), pws, nws, st), "tlc_ckpt8_norm_grad")
+        return o, g
+    return _on_stream(device, stream, body)
+
+
+def ckpt8_weight_grad_workspace_size(rows: int, n: int, cols: int) -> int:
+    return int(lib().tlc_ckpt8_weight_grad_workspace_size(rows, n, cols))
+
+
+def ckpt8_weight_grad(dy: torch.Tensor, x: Checkpoint8, *, col_scale: torch.Tensor | None = None,
+                      dw: torch.Tensor | None = None, accumulate: bool = False, workspace=None,
+                      stream=None) -> torch.Tensor:
+    """dw[n, cols] (float32) = dy^T x (times col_scale per column), x the
+    checkpoint's values; with `accumulate` added to dw, which may be a view
+    into a flat gradient buffer."""
+    pd, sd = _matrix(dy, "dy")
+    rows, n = dy.shape
+    cols, device = x.cols, dy.device
+    pc, ps = _checkpoint(x, "x", rows, cols, device)
+    pcs, cdt = _vector(col_scale, cols, device, "col_scale")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+
+    def body(st):
+        g = dw if dw is not None else torch.empty((n, cols), dtype=torch.float32, device=device)
+        pg, sg = _matrix(g, "dw")
+        if g.dtype != torch.float32 or g.shape[0] != n or g.shape[1] != cols or g.device != device:
+            raise ValueError(f"dw must be ({n}, {cols}) of float32 on {device}")
+        ws = _ckpt8_workspace(ckpt8_weight_grad_workspace_size(rows, n, cols), device, workspace)
+        _check(lib().tlc_ckpt8_weight_grad(pd, sd, _DTYPES[dy.dtype], rows, n, x.format, pc, ps, cols, pcs, cdt, pg,
+                                           sg, int(accumulate), ws.data_ptr(), ws.numel(), st),
+               "tlc_ckpt8_weight_grad")
+        return g
+    return _on_stream(device, stream, body)
 
 
 def gather_probe(src: torch.Tensor, idx: torch.Tensor, dst: torch.Tensor, stream=None):

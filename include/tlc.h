@@ -415,6 +415,124 @@ int tlc_planes_gather(const float* src, const uint64_t* src_off, float* dst, con
 int tlc_planes_scatter(const float* src, const uint64_t* src_off, float* dst, const uint64_t* dst_off,
                        const uint64_t* n, uint32_t count, uint64_t max_n, tlc_stream_t stream);
 
+/* ---- 8-bit checkpoints of activations ---------------------------------------
+ * What a backward pass needs of the forward pass, kept in 8 bits, and the
+ * backward steps that read it: they end in the fp32 gradients that the calls
+ * above compress.  The review pages have no such step; the definitions are
+ * this library's.
+ *
+ * A checkpoint of a matrix [rows, cols] is a byte per value and a scale byte
+ * per group of 32 consecutive columns of a row (the last group may be short):
+ *   codes   uint8[rows][tlc_ckpt8_code_stride(cols)],   16-byte aligned;
+ *   scales  uint8[rows][tlc_ckpt8_scale_stride(cols)],  4-byte aligned.
+ * Bytes past a row's columns and groups are written as 0 and not read.
+ * A scale byte b stands for 2^(b-127) and a code for a number times it:
+ *   TLC_CKPT8_INT8  the byte as a two's complement integer, -127..127 (C = 127);
+ *   TLC_CKPT8_E4M3  the byte as an 8-bit float of sign, 4 exponent bits (bias
+ *                   7) and 3 fraction bits, no infinities (C = 448).
+ * With amax the group's largest magnitude, the scale is 2^e for the least e
+ * with amax <= C*2^e, held to -126 <= e <= 121 (INT8) or -117 <= e <= 119
+ * (E4M3); a code is the nearest one to x*2^-e, ties to even, and values past
+ * the largest code take it.  Every value a checkpoint stands for is 0 or a
+ * normal, finite bfloat16 number.  A group of zeros has scale byte 0.  A group
+ * with an infinity or a NaN has scale byte 255 and codes 0, and each of its
+ * values decodes to NaN.
+ *
+ * Matrices are row-major; consecutive columns are adjacent and rows lie a
+ * stride (in elements, >= cols) apart, at any element: no alignment beyond the
+ * element's is asked.  rows may be 0 (the call then writes nothing, except
+ * where said otherwise); 1 <= cols and rows, cols, strides <= 2^31 - 1.
+ * dtypes are enum tlc_dtype.  Arithmetic is fp32 or wider; each output is
+ * rounded once, to nearest even.  Outputs must not overlap inputs or each
+ * other unless said otherwise.  No call here has a status word: nothing in the
+ * data can be refused.  Workspaces as above (device, 256-byte aligned, size
+ * from the *_workspace_size call, host only, 0 for sizes out of range). */
+enum tlc_dtype { TLC_F32 = 0, TLC_F16 = 1, TLC_BF16 = 2 };
+enum tlc_ckpt8_format { TLC_CKPT8_INT8 = 1, TLC_CKPT8_E4M3 = 2 };
+/* f(x): x*Phi(x); its form with tanh(sqrt(2/pi)*(x + 0.044715 x^3)); x/(1+e^-x) */
+enum tlc_activation { TLC_ACT_GELU = 1, TLC_ACT_GELU_TANH = 2, TLC_ACT_SILU = 3 };
+
+/* Bytes between the rows of a checkpoint's codes (32 per group) and of its
+ * scales (one per group, up to a multiple of 4).  Host only; 0 for cols out of
+ * range. */
+uint64_t tlc_ckpt8_code_stride(uint64_t cols);
+uint64_t tlc_ckpt8_scale_stride(uint64_t cols);
+
+/* Checkpoint of x[rows, cols]. */
+int tlc_ckpt8_pack(const void* x, uint64_t x_stride, int dtype, uint64_t rows, uint64_t cols, int format,
+                   uint8_t* codes, uint8_t* scales, tlc_stream_t stream);
+
+/* The values a checkpoint stands for: exact in fp32 and bf16, rounded in fp16
+ * (magnitudes past its largest become infinite). */
+int tlc_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int format, uint64_t rows, uint64_t cols, void* y,
+                     uint64_t y_stride, int dtype, tlc_stream_t stream);
+
+/* y = f(a), or y = f(a)*b where b is given, and the checkpoints of a (and b),
+ * in one pass.  a, b and y have the same dtype; a and b may be halves of one
+ * wider matrix.  b_codes and b_scales are given exactly where b is. */
+int tlc_ckpt8_act(int act, const void* a, uint64_t a_stride, const void* b, uint64_t b_stride, int dtype,
+                  uint64_t rows, uint64_t cols, void* y, uint64_t y_stride, int format, uint8_t* a_codes,
+                  uint8_t* a_scales, uint8_t* b_codes, uint8_t* b_scales, tlc_stream_t stream);
+
+/* The gradient of that y from the checkpoints, with a and b their values:
+ *   da = dy*f'(a) (times b),  db = dy*f(a),
+ * and, where y_codes and y_scales are given, the checkpoint of f(a) (times b)
+ * in fp32, for the weight gradient of the layer that read y.  db, b_codes and
+ * b_scales are given together or not at all.  da or db may be dy itself (same
+ * pointer and stride). */
+int tlc_ckpt8_act_grad(int act, const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                       const uint8_t* b_scales, int format, const void* dy, uint64_t dy_stride, int dtype,
+                       uint64_t rows, uint64_t cols, void* da, uint64_t da_stride, void* db, uint64_t db_stride,
+                       uint8_t* y_codes, uint8_t* y_scales, tlc_stream_t stream);
+
+/* Root-mean-square norm of a residual stream:
+ *   sum  = x + residual, rounded to dtype (residual NULL: sum = x, and `sum`
+ *          must be NULL); optional; may be x or residual itself (same pointer
+ *          and stride);
+ *   rstd = (mean of sum^2 over the row + eps)^(-1/2), fp32[rows], optional;
+ *   n    = sum * rstd;   y = n * weight, optional; weight[cols] of the same dtype
+ *          or fp32 (NULL: 1);
+ *   codes, scales: the checkpoint of n (weighted 0: what the gradients below
+ *          take) or of n*weight (weighted 1: an 8-bit input for the next
+ *          product), from n in 64 bits; given together or not at all.
+ * One of y and codes at least.  cols <= 32768; eps > 0 and finite.  The squares
+ * are summed in 64 bits. */
+int tlc_ckpt8_norm(const void* x, uint64_t x_stride, const void* residual, uint64_t residual_stride, int dtype,
+                   uint64_t rows, uint64_t cols, const void* weight, int weight_dtype, float eps, int weighted,
+                   void* sum, uint64_t sum_stride, void* y, uint64_t y_stride, int format, uint8_t* codes,
+                   uint8_t* scales, float* rstd, tlc_stream_t stream);
+
+/* Its gradient, with n either the values of the (unweighted) checkpoint or, if
+ * codes and scales are NULL, sum*rstd:
+ *   g  = dy * weight,   dx = dsum + rstd*(g - n * mean of g*n over the row),
+ *   dw[c] = sum over rows of dy*n (added to dw[c] with accumulate != 0).
+ * dx is the gradient of x and of residual alike; dsum, the gradient that
+ * reaches `sum` from elsewhere, is optional; dx may be dy or dsum itself (same
+ * pointer and stride).  rstd as tlc_ckpt8_norm wrote it.  dw (fp32[cols]) is
+ * optional; the workspace is needed for it only.  rows == 0: dw becomes 0, or
+ * stays with accumulate.  The order of every sum is fixed. */
+size_t tlc_ckpt8_norm_grad_workspace_size(uint64_t rows, uint64_t cols);
+int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, uint64_t dsum_stride, int dtype,
+                        uint64_t rows, uint64_t cols, const void* sum, uint64_t sum_stride, int format,
+                        const uint8_t* codes, const uint8_t* scales, const float* rstd, const void* weight,
+                        int weight_dtype, void* dx, uint64_t dx_stride, float* dw, int accumulate, void* workspace,
+                        size_t workspace_bytes, tlc_stream_t stream);
+
+/* Weight gradient of a linear layer whose input is kept as a checkpoint x:
+ *   dw[i][c] = col_scale[c] * sum over rows t of dy[t][i]*x[t][c]
+ * (added to dw[i][c] with accumulate != 0), dy[rows, n], dw fp32[n][cols] with
+ * rows dw_stride apart, for example a tensor's place in the flat buffer that
+ * tlc_compress_group reads.  col_scale[cols], of dy's dtype or fp32, is
+ * optional: the weight of the norm whose unweighted checkpoint x is.  Products are exact (dy
+ * as one, two or three bfloat16 numbers for bf16, fp16, fp32), sums fp32 in a
+ * fixed order.  rows == 0: dw becomes 0, or stays with accumulate.
+ * TLC_ERR_INVALID_ARG also for n and cols of more than 2^30 tiles of 128 x 128. */
+size_t tlc_ckpt8_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols);
+int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
+                          const uint8_t* codes, const uint8_t* scales, uint64_t cols, const void* col_scale,
+                          int col_scale_dtype, float* dw, uint64_t dw_stride, int accumulate, void* workspace,
+                          size_t workspace_bytes, tlc_stream_t stream);
+
 /* ---- measurement helpers (not part of the codec) -------------------------- */
 
 /* Streaming copy of `bytes` bytes (a multiple of 16, both pointers 16-byte
