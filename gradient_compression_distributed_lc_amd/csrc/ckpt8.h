@@ -55,10 +55,11 @@ struct Raw8 {
     u4 w[T::kVecs];
 };
 
-// The first n (1..8) of the eight values at p, the rest 0.
+// The first n (at most 8) of the eight values at p, the rest 0.  `whole`: n is
+// 8 or 0.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const typename T::Elem* p, int n) {
-    Raw8<T> r;
+__device__ __forceinline__ Raw8<T> load8(const typename T::Elem* p, int n, bool whole = false) {
+    Raw8<T> r = {};
     if (n >= 8) {
         if constexpr (T::kVecs == 2) {
             r.w[0] = *reinterpret_cast<const u4_at4*>(p);
@@ -66,7 +67,7 @@ __device__ __forceinline__ Raw8<T> load8(const typename T::Elem* p, int n) {
         } else {
             r.w[0] = *reinterpret_cast<const u4_at2*>(p);
         }
-    } else {
+    } else if (!whole) {
         if constexpr (T::kVecs == 2) {
             const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll

@@ -5,6 +5,7 @@
 // exact and the sums are the matrix cores' fp32.
 
 #include <algorithm>
+#include <cmath>
 
 #include "ckpt8.h"
 #include "launch.h"
@@ -15,7 +16,6 @@ using namespace tlc_ckpt8;
 using tlc_internal::launch;
 
 constexpr int kThreads = 256;  // four wavefronts, two by two
-constexpr int kStep = 32;      // rows of dy and x a block takes at a time
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
@@ -32,10 +32,18 @@ struct MatArgs {
     int accumulate;
     float* dw;           // with one slice
     uint64_t dw_stride;
-    float* partial;      // [slices][n][cols], else nullptr
-    uint64_t slice_rows; // rows of one slice, a multiple of kStep
+    f4* partial;         // with several: [slices][tiles], each tile as its lanes hold it; else nullptr
+    uint64_t slice_rows; // rows of one slice, a multiple of 64
     uint32_t tiles, tiles_i, tiles_c;  // tiles of dw, its rows of them, and those of one row
 };
+
+// Place in the matrix of tile number `tile`: neighbours in bands of 4 rows of tiles.
+__device__ __forceinline__ void tile_place(const MatArgs& p, uint32_t tile, uint32_t* i, uint32_t* c) {
+    const uint32_t band = tile / (4 * p.tiles_c), in_band = tile % (4 * p.tiles_c);
+    const uint32_t band_rows = min(4u, p.tiles_i - band * 4);
+    *i = band * 4 + in_band % band_rows;
+    *c = in_band / band_rows;
+}
 
 // v as a sum of bfloat16 numbers, each the leading bits of what is left.
 template <int kTerms>
@@ -85,19 +93,23 @@ __device__ __forceinline__ float column_scale(const void* p, uint32_t c) {
 // each gets 4 rows of one column.  Which 8 of the 16 rows a lane holds is the
 // same for both operands, so their order does not matter.
 //
-// LDS: 32-byte segments (16 columns) of row t lie at segment ^ (t & 3), so that
-// the 4 rows of one transposing read fall into different banks (measured: 105
-// bytes a clock and CU instead of 32).
+// LDS: the 16-byte slots (8 columns) of row t lie at slot ^ swizzle(t).  The 4
+// rows x 32 columns that half a wavefront reads at once then fall into the 64
+// banks once each, and so do the slots that 8 lanes write at once (8 lanes
+// hold 4 units of codes of two rows).  Without it both take two to four times
+// as long (counted: 2 clocks a read and 8 a 16-byte write, no conflicts).
 //
 // Two stages.  While one is multiplied, the rows loaded before go to the other
 // and the next ones are on their way in registers.  The block meets once a
 // step, before the last products, whose operands it has then read; these run
 // while the next stage's first operands are read.
-template <int kTerms, int kTile>
+template <int kTerms, int kTile, int kStep>
 struct __align__(16) Stage {
     uint16_t a[kTerms][kStep][kTile];
     uint16_t b[kStep][kTile];
 };
+
+__device__ __forceinline__ int swizzle(int t) { return (t & 3) << 2 | (t & 1); }
 
 __device__ __forceinline__ s4v read_tr(const uint16_t* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p);
@@ -110,13 +122,13 @@ __device__ __forceinline__ b8v operand(const uint16_t* p) {
     return __builtin_bit_cast(b8v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// The order of instructions in a region of kGroups times 16 products: a
+// The order of instructions in a region of kProducts products: a
 // product keeps the matrix core busy for 32 clocks, in which the wavefront can
 // issue about seven others.
-template <int kGroups>
+template <int kProducts>
 __device__ __forceinline__ void interleave() {
 #pragma unroll
-    for (int i = 0; i < kGroups * 16; ++i) {
+    for (int i = 0; i < kProducts; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // vector arithmetic
@@ -125,8 +137,8 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <typename T, typename W, int FMT, int kTile>
-__global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
+template <typename T, typename W, int FMT, int kTile, int kStep>
+__global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(MatArgs p) {
     using Elem = typename T::Elem;
     constexpr int kTerms = T::kTerms;
     constexpr int kWave = kTile / 2, kTiles = kWave / 32;
@@ -134,37 +146,42 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
     constexpr int kLoadsA = kStep * kUnits / kThreads;         // of them a lane
     constexpr int kLoadsB = kStep * kTile / 16 / kThreads;     // 16-byte units of codes a lane
     static_assert(kLoadsA >= 1 && kLoadsB >= 1, "too narrow a tile");
-    __shared__ Stage<kTerms, kTile> stage0, stage1;
+    using Buffer = Stage<kTerms, kTile, kStep>;
+    __shared__ Buffer stage0, stage1;
 
-    // neighbouring tiles on one XCD (blocks go round the 8 of them), in bands of 4 rows of tiles
+    // neighbouring tiles on one XCD: blocks go round the 8 of them
     uint32_t b = blockIdx.x;
     const uint32_t total = gridDim.x, per = total / 8;
     if (b < per * 8) b = b % 8 * per + b / 8;
     const uint32_t slice = b / p.tiles, tile = b % p.tiles;
-    const uint32_t band = tile / (4 * p.tiles_c), in_band = tile % (4 * p.tiles_c);
-    const uint32_t band_rows = min(4u, p.tiles_i - band * 4);
-    const uint32_t i0 = (band * 4 + in_band % band_rows) * kTile, c0 = in_band / band_rows * kTile;
+    uint32_t tile_i, tile_c;
+    tile_place(p, tile, &tile_i, &tile_c);
+    const uint32_t i0 = tile_i * kTile, c0 = tile_c * kTile;
     const uint64_t t_begin = slice * p.slice_rows, t_end = min(p.rows, t_begin + p.slice_rows);
     const int steps = (int)((t_end - t_begin + kStep - 1) / kStep);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 
     // what the lane loads: rows ra + i*(rows between), columns from i0 + 8*ua; codes likewise
     const int ra = threadIdx.x / kUnits, ua = threadIdx.x % kUnits;
-    const int rb = threadIdx.x / (kTile / 16), ub = threadIdx.x % (kTile / 16);
+    // (codes: 4 neighbouring units of two rows in 8 lanes)
+    const int pair = threadIdx.x / (kTile / 8), in_pair = threadIdx.x % (kTile / 8);
+    const int rb = 2 * pair + (in_pair >> 2 & 1), ub = (in_pair & 3) | in_pair >> 3 << 2;
     constexpr int kRowsA = kThreads / kUnits, kRowsB = kThreads / (kTile / 16);
     // A lane past the last column loads the row's first ones, and a unit that
     // ends past it runs on into the next row: those columns of the operands
-    // only reach values of dw that are not stored.  Only the last row may not
-    // be read past its end, and rows past t_end have to be zeros.
+    // only reach values of dw that are not stored.  Only at the matrix's end
+    // may a unit not run on, and rows past t_end have to be zeros.
     const int count = min(max((int)(p.n - i0) - ua * 8, 0), 8);
     const Elem* const pa =
         static_cast<const Elem*>(p.dy) + (t_begin + ra) * p.dy_stride + (count ? i0 + ua * 8 : 0);
     const uint32_t cb = c0 + ub * 16 < p.code_row ? c0 + ub * 16 : 0;
     const uint8_t* const pb = p.codes + (t_begin + rb) * p.code_row + cb;
     const uint8_t* const ps = p.scales + (t_begin + rb) * p.scale_row + cb / 32;
-    const uint64_t here = t_end - t_begin;
-    // steps all of whose rows are here and not the matrix's last one
-    const int whole = p.dy_stride >= 8 ? (int)((t_end == p.rows ? here - 1 : here) / kStep) : 0;
+    const int here = (int)(t_end - t_begin);
+    // rows from whose every unit eight columns can be read: all but the last ceil(8 / stride)
+    const int tail = p.dy_stride >= 8 ? 1 : (int)((7 + p.dy_stride) / p.dy_stride);
+    const int safe = t_end + tail > p.rows ? max(here - (int)(t_end + tail - p.rows), 0) : here;
+    const int whole = safe / kStep;  // steps of such rows only
 
     // In registers: what was loaded for the two steps after the next (an even
     // and an odd one), and the next step's codes as bfloat16 numbers.
@@ -186,21 +203,30 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
     };
     auto load = [&](Loaded& g, int s) {
         if (s < whole) return load_whole(g, s);
-        const uint64_t t = (uint64_t)s * kStep;
-        const uint64_t left = here - t;  // rows from this step on
+        const int t = s * kStep;
+        int alone = -1;  // a row of this lane that has to be read one by one
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
-            const int r = i * kRowsA;
-            g.a[i] = load8<T>(pa + (t + r) * p.dy_stride, (uint64_t)(ra + r) < left ? count : 0);
+            const int r = t + ra + i * kRowsA;
+            const bool run_on = r < safe || (r < here && count == 8);
+            g.a[i] = load8<T>(pa + (uint64_t)(t + i * kRowsA) * p.dy_stride, run_on ? 8 : 0, true);
+            if (!run_on && r < here) alone = i;
+        }
+        static_assert(kRowsA >= 8, "a lane has at most one of the last eight rows");
+        if (alone >= 0) {
+            const Raw8<T> v = load8<T>(pa + (uint64_t)(t + alone * kRowsA) * p.dy_stride, min(count, 7));
+#pragma unroll
+            for (int i = 0; i < kLoadsA; ++i)
+                if (i == alone) g.a[i] = v;
         }
 #pragma unroll
         for (int i = 0; i < kLoadsB; ++i) {
-            const int r = i * kRowsB;
+            const uint64_t r = t + i * kRowsB;
             g.codes[i] = u4{0, 0, 0, 0};
             g.byte[i] = 0;
-            if ((uint64_t)(rb + r) < left) {
-                g.codes[i] = *reinterpret_cast<const u4*>(pb + (t + r) * p.code_row);
-                g.byte[i] = ps[(t + r) * p.scale_row];
+            if ((int)r + rb < here) {
+                g.codes[i] = *reinterpret_cast<const u4*>(pb + r * p.code_row);
+                g.byte[i] = ps[r * p.scale_row];
             }
         }
     };
@@ -208,10 +234,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
 #pragma unroll
         for (int i = 0; i < kLoadsB; ++i) decode16<FMT>(g.codes[i], g.byte[i], gx[i]);
     };
-    auto store = [&](Stage<kTerms, kTile>& st, const Loaded& g) {
+    auto store = [&](Buffer& st, const Loaded& g) {
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
-            const int r = ra + i * kRowsA, at = ((ua >> 1) ^ (r & 3)) * 16 + (ua & 1) * 8;
+            const int r = ra + i * kRowsA, at = (ua ^ swizzle(r)) * 8;
             if constexpr (kTerms == 1) {
                 *reinterpret_cast<u4*>(&st.a[0][r][at]) = g.a[i].w[0];
             } else {
@@ -232,30 +258,34 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
         }
 #pragma unroll
         for (int i = 0; i < kLoadsB; ++i) {
-            const int r = rb + i * kRowsB, at = (ub ^ (r & 3)) * 16;
+            const int r = rb + i * kRowsB, at = (2 * ub ^ swizzle(r)) * 8;
             *reinterpret_cast<u4*>(&st.b[r][at]) = gx[i][0];
-            *reinterpret_cast<u4*>(&st.b[r][at + 8]) = gx[i][1];
+            *reinterpret_cast<u4*>(&st.b[r][at ^ 8]) = gx[i][1];
         }
     };
 
-    // the lane's place in an operand: rows lane/32*8 + (lane%16)/4, segment + lane/16%2, 4 columns of lane%4
-    const int sub = (lane >> 2) & 3, seg = (lane >> 4) & 1;
+    // the lane's place in an operand of each 32 columns: row lane/32*8 + (lane%16)/4,
+    // columns lane/16%2*16 + lane%4*4, four of them
     const int wi = (wave >> 1) * kWave, wc = (wave & 1) * kWave;
-    const int row = (lane >> 5) * 8 + sub;
-    int place[2];  // of an even and an odd 32-column tile: the segments' low bits differ
+    const int row = (lane >> 5) * 8 + (lane >> 2 & 3);
+    int place_a[kTiles], place_b[kTiles];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) place[q] = row * kTile + (((2 * q + seg) ^ sub) * 16) + (lane & 3) * 4;
+    for (int q = 0; q < kTiles; ++q) {
+        const int slot = q * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
+        place_a[q] = row * kTile + ((wi / 8 + slot) ^ swizzle(row)) * 8 + (lane & 1) * 4;
+        place_b[q] = row * kTile + ((wc / 8 + slot) ^ swizzle(row)) * 8 + (lane & 1) * 4;
+    }
 
     f16v acc[kTiles][kTiles] = {};
-    auto operands_b = [&](const Stage<kTerms, kTile>& st, int k, b8v* f) {
+    auto operands_b = [&](const Buffer& st, int k, b8v* f) {
 #pragma unroll
         for (int c = 0; c < kTiles; ++c)
-            f[c] = operand<kTile>(&st.b[0][0] + k * 16 * kTile + place[c & 1] + wc + (c & ~1) * 32);
+            f[c] = operand<kTile>(&st.b[0][0] + k * 16 * kTile + place_b[c]);
     };
-    auto operands_a = [&](const Stage<kTerms, kTile>& st, int k, int term, b8v* f) {
+    auto operands_a = [&](const Buffer& st, int k, int term, b8v* f) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
-            f[i] = operand<kTile>(&st.a[term][0][0] + k * 16 * kTile + place[i & 1] + wi + (i & ~1) * 32);
+            f[i] = operand<kTile>(&st.a[term][0][0] + k * 16 * kTile + place_a[i]);
     };
     auto multiply = [&](const b8v* fa, const b8v* fb) {
 #pragma unroll
@@ -265,131 +295,173 @@ __global__ __launch_bounds__(kThreads, 1) void k_weight_grad(MatArgs p) {
                 acc[i][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[c], acc[i][c], 0, 0, 0);
     };
 
+    // A step is kSubs times 16 rows, each of kTerms products of the wavefront's
+    // tile.  The operands of the next product are read while one runs; those of
+    // the step's last product are in registers when the block meets.
+    constexpr int kSubs = kStep / 16, kRounds = kSubs * kTerms;
     b8v fa[2][kTiles], fb[2][kTiles];
+    auto round = [&](const Buffer& now, int q) {  // product q, and the reads for q + 1
+        if (q % kTerms == 0 && q / kTerms + 1 < kSubs) operands_b(now, q / kTerms + 1, fb[(q / kTerms + 1) & 1]);
+        operands_a(now, (q + 1) / kTerms, (q + 1) % kTerms, fa[(q + 1) & 1]);
+        multiply(fa[q & 1], fb[q / kTerms & 1]);
+    };
     // Step s: multiplies `now`, stores step s+1 to `next`, loads step s+3 into
     // the registers that frees, and decodes the codes of step s+2.  kMain: all
     // of it without a branch, so that one schedule spans the products and
     // everything else.
-    auto step = [&](Stage<kTerms, kTile>& now, Stage<kTerms, kTile>& next, Loaded& here_g, Loaded& next_g, int s,
-                    auto main) {
+    auto step = [&](Buffer& now, Buffer& next, Loaded& here_g, Loaded& next_g, int s, auto main) {
         constexpr bool kMain = decltype(main)::value;
-        operands_b(now, 1, fb[1]);
-#pragma unroll
-        for (int k = 0; k < kTerms; ++k) {
-            operands_a(now, k + 1 < kTerms ? 0 : 1, (k + 1) % kTerms, fa[(k + 1) & 1]);
-            multiply(fa[k & 1], fb[0]);
-        }
-        if (kMain || s + 1 < steps) store(next, next_g);
+        if (kMain || s >= 0) round(now, 0);
+        if (kMain || (s + 1 >= 0 && s + 1 < steps)) store(next, next_g);
         if constexpr (kMain)
             load_whole(next_g, s + 3);
-        else if (s + 3 < steps)
+        else if (s + 3 >= 0 && s + 3 < steps)
             load(next_g, s + 3);
+        if (kMain || s >= 0) {
 #pragma unroll
-        for (int k = 0; k + 1 < kTerms; ++k) {
-            operands_a(now, 1, k + 1, fa[(kTerms + k + 1) & 1]);
-            multiply(fa[(kTerms + k) & 1], fb[1]);
+            for (int q = 1; q + 1 < kRounds; ++q) round(now, q);
         }
-        if constexpr (kMain && kTiles == 4) interleave<kTerms * 2 - 1>();
+        if constexpr (kMain) interleave<kTiles * kTiles * (kRounds - 1)>();
         __syncthreads();
-        b8v last[kTiles];
+        b8v last_a[kTiles], last_b[kTiles];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) last[i] = fa[(2 * kTerms - 1) & 1][i];
-        if (kMain || s + 1 < steps) {
+        for (int i = 0; i < kTiles; ++i) last_a[i] = fa[(kRounds - 1) & 1][i], last_b[i] = fb[(kSubs - 1) & 1][i];
+        if (kMain || (s + 1 >= 0 && s + 1 < steps)) {
             operands_a(next, 0, 0, fa[0]);
             operands_b(next, 0, fb[0]);
         }
-        multiply(last, fb[1]);
-        if (kMain || s + 2 < steps) decode(here_g);
-        if constexpr (kMain && kTiles == 4) interleave<1>();
+        if (kMain || s >= 0) multiply(last_a, last_b);
+        if (kMain || (s + 2 >= 0 && s + 2 < steps)) decode(here_g);
+        if constexpr (kMain) interleave<kTiles * kTiles>();
     };
-    if (steps > 0) {
-        load(g0, 0);
-        decode(g0);
-        store(stage0, g0);
-        if (steps > 1) {
-            load(g1, 1);
-            decode(g1);
-        }
-        if (steps > 2) load(g0, 2);
-        __syncthreads();
-        operands_a(stage0, 0, 0, fa[0]);
-        operands_b(stage0, 0, fb[0]);
-        int s = 0;
-        for (; s + 4 < whole; s += 2) {
-            step(stage0, stage1, g0, g1, s, Int<1>{});
-            step(stage1, stage0, g1, g0, s + 1, Int<1>{});
-        }
-#pragma unroll 1
-        for (; s < steps; s += 2) {
-            step(stage0, stage1, g0, g1, s, Int<0>{});
-            if (s + 1 < steps) step(stage1, stage0, g1, g0, s + 1, Int<0>{});
-        }
+    // The steps before 0 fill the pipeline; they and the last ones are one loop.
+    for (int s = -4; s < steps; s += 2) {
+        if (s >= 0)
+            for (; s + 4 < whole; s += 2) {
+                step(stage0, stage1, g0, g1, s, Int<1>{});
+                step(stage1, stage0, g1, g0, s + 1, Int<1>{});
+            }
+        step(stage0, stage1, g0, g1, s, Int<0>{});
+        if (s + 1 < steps) step(stage1, stage0, g1, g0, s + 1, Int<0>{});
     }
 
     // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32
-    const uint32_t row0 = i0 + wi + (lane >> 5) * 4, col0 = c0 + wc + (lane & 31);
-    const bool direct = p.partial == nullptr;
-    float* const out = direct ? p.dw : p.partial + (uint64_t)slice * p.n * p.cols;
-    const uint64_t stride = direct ? p.dw_stride : p.cols;
-    float cs[kTiles];
-#pragma unroll
-    for (int c = 0; c < kTiles; ++c)
-        cs[c] = column_scale<W>(direct ? p.col_scale : nullptr, min(col0 + c * 32, p.cols - 1));
-    const bool add = direct && p.accumulate;
-    auto write = [&](auto edge) {
-        constexpr bool kEdge = decltype(edge)::value;
+    if (p.partial) {  // four rows a store, each lane's registers side by side: the sum's business to sort out
+        f4* const out = p.partial + (uint64_t)b * (kTile * kTile / 4) + wave * (kTile * kTile / 16) + lane;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t r = row0 + i * 32 + (j >> 2) * 8 + (j & 3);
-                float* const o = out + r * stride + col0;
-                if (!kEdge || r < p.n) {
+            for (int c = 0; c < kTiles; ++c)
 #pragma unroll
-                    for (int c = 0; c < kTiles; ++c)
-                        if (!kEdge || col0 + c * 32 < p.cols) {
-                            const float v = acc[i][c][j] * cs[c];
-                            o[c * 32] = kEdge && add ? o[c * 32] + v : v;
-                        }
-                }
+                for (int j = 0; j < 4; ++j)
+                    out[((i * kTiles + c) * 4 + j) * 64] = f4{acc[i][c][4 * j], acc[i][c][4 * j + 1],
+                                                              acc[i][c][4 * j + 2], acc[i][c][4 * j + 3]};
+        return;
+    }
+    const uint32_t row0 = i0 + wi + (lane >> 5) * 4, col0 = c0 + wc + (lane & 31);
+    float cs[kTiles];
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c) cs[c] = column_scale<W>(p.col_scale, min(col0 + c * 32, p.cols - 1));
+    if (i0 + kTile <= p.n && c0 + kTile <= p.cols && !p.accumulate) {
+        float* const o = p.dw + row0 * p.dw_stride + col0;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int c = 0; c < kTiles; ++c)
+                    o[(i * 32 + (j >> 2) * 8 + (j & 3)) * p.dw_stride + c * 32] = acc[i][c][j] * cs[c];
+        return;
+    }
+    // An edge, or dw is added to: 32 rows at a time through LDS and a short
+    // loop.  (Straight code for it is 20 KB that run once, and took 25 us to
+    // fetch.)
+    float* const wave_out = reinterpret_cast<float*>(wave < 2 ? &stage0 : &stage1) + (wave & 1) * 32 * kWave;
+    static_assert(sizeof(Buffer) >= 2 * 32 * kWave * sizeof(float), "two wavefronts' rows fit a stage");
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+                wave_out[((lane >> 5) * 4 + (j >> 2) * 8 + (j & 3)) * kWave + (lane & 31) + c * 32] =
+                    acc[i][c][j] * cs[c];
+        __syncthreads();
+#pragma unroll 4
+        for (int e = lane; e < 32 * kWave; e += 64) {
+            const uint32_t r = i0 + wi + i * 32 + e / kWave, c = c0 + wc + e % kWave;
+            if (r < p.n && c < p.cols) {
+                float* const o = p.dw + r * p.dw_stride + c;
+                *o = p.accumulate ? *o + wave_out[e] : wave_out[e];
             }
-    };
-    if (i0 + kTile <= p.n && c0 + kTile <= p.cols && !add)
-        write(Int<0>{});
-    else
-        write(Int<1>{});
+        }
+    }
 }
 
 // dw (+)= col_scale * the slices' sums, added in order; no slices: 0.
 template <typename W>
-__global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t slices) {
-    const uint64_t per_row = (p.cols + kThreads - 1) / kThreads;
-    for (uint64_t b = blockIdx.x; b < per_row * p.n; b += gridDim.x) {
-        const uint64_t row = b / per_row;
-        const uint32_t c = (uint32_t)(b - row * per_row) * kThreads + threadIdx.x;
-        if (c >= p.cols) continue;
-        float s = 0.0f;
-        for (uint32_t k = 0; k < slices; ++k) s += p.partial[((uint64_t)k * p.n + row) * p.cols + c];
-        s *= column_scale<W>(p.col_scale, c);
-        float* const o = p.dw + row * p.dw_stride + c;
-        *o = p.accumulate ? *o + s : s;
+__global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t slices, uint32_t tile_size) {
+    const uint32_t per = tile_size * tile_size / 4;  // f4 of a tile
+    const uint32_t tile = blockIdx.x / (per / kThreads), v = blockIdx.x % (per / kThreads) * kThreads + threadIdx.x;
+    const f4* const in = p.partial + (uint64_t)tile * per + v;
+    const uint64_t next = (uint64_t)p.tiles * per;
+    f4 s = {};
+    uint32_t k = 0;
+    for (; k + 4 <= slices; k += 4) {
+        const f4 a = in[k * next], b = in[(k + 1) * next], c = in[(k + 2) * next], d = in[(k + 3) * next];
+        s += a;
+        s += b;
+        s += c;
+        s += d;
     }
+    for (; k < slices; ++k) s += in[k * next];
+    uint32_t ti, tc;
+    tile_place(p, tile, &ti, &tc);
+    // the lane's place in the product: wavefront, 32x32 part, four rows of one column
+    const uint32_t parts = tile_size / 64, lane = v % 64, part = v / 256 % (parts * parts), wave = v / (per / 4);
+    const uint32_t row = ti * tile_size + (wave >> 1) * (tile_size / 2) + part / parts * 32 + v / 64 % 4 * 8 +
+                         (lane >> 5) * 4;
+    const uint32_t col = tc * tile_size + (wave & 1) * (tile_size / 2) + part % parts * 32 + (lane & 31);
+    if (col >= p.cols) return;
+    const float cs = column_scale<W>(p.col_scale, col);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (row + j < p.n) {
+            float* const o = p.dw + (row + j) * p.dw_stride + col;
+            *o = p.accumulate ? *o + s[j] * cs : s[j] * cs;
+        }
 }
 
-// Slices of the rows: enough blocks for the chip, none below 256 rows.
+// The tile and into how many slices the rows are cut, by the least of an
+// estimate in microseconds.  Measured: 32 rows of a 256x256 tile take 0.8 us a
+// bfloat16 term of dy, one block a CU; of a 128x128 tile 0.43 us, or 0.7 us
+// with two blocks on a CU.  Slices fill the chip where the tiles do not (or
+// leave a last round mostly empty) and cost writing and reading their sums.
+// bf16, e4m3: 16384x4096x4096 takes 430 us in tiles of 256 and 580 in tiles of
+// 128, 4096x4096x1024 (64 tiles of 256 in 4 slices) 62 and 58, 2048x2048x2048
+// 47 and 31, 512x1024x4096 34 and 13; 8192x1024x1024 in tiles of 128 takes 94
+// in one slice and 36 in four.
 struct Shape {
     uint32_t tile, slices;
     uint64_t slice_rows, tiles_i, tiles_c;
 };
-Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols) {
-    Shape s;
-    s.tile = 256;
-    s.tiles_i = (n + s.tile - 1) / s.tile, s.tiles_c = (cols + s.tile - 1) / s.tile;
-    const uint64_t tiles = s.tiles_i * s.tiles_c;
-    const uint64_t want = std::min<uint64_t>((256 + tiles - 1) / tiles, std::max<uint64_t>(rows / 256, 1));
-    s.slice_rows = ((rows + want - 1) / want + kStep - 1) / kStep * kStep;
-    s.slices = s.slice_rows ? (uint32_t)((rows + s.slice_rows - 1) / s.slice_rows) : 0;
-    return s;
+Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms) {
+    Shape best = {};
+    double least = 0.0;
+    for (uint32_t tile = 128; tile <= 256; tile *= 2) {
+        const uint64_t ti = (n + tile - 1) / tile, tc = (cols + tile - 1) / tile;
+        for (uint64_t k = 1; k <= 32 && (k == 1 || rows / k >= 128); ++k) {
+            const uint64_t cut = ((rows + k - 1) / k + 63) / 64 * 64, slices = cut ? (rows + cut - 1) / cut : 0;
+            const double blocks = (double)ti * (double)tc * (double)slices;
+            const double step = tile == 256 ? 0.8 * std::ceil(blocks / 256)
+                                            : blocks <= 256 ? 0.43 : 0.7 * std::ceil(blocks / 512);
+            double us = step * terms * (double)(cut / 32);
+            if (slices > 1) us += 4.0 + (2.0 * slices + 1.0) * (double)n * (double)cols * 4.0 / 5.5e6;
+            if (!best.tile || us < least) best = {tile, (uint32_t)slices, cut, ti, tc}, least = us;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -398,9 +470,13 @@ extern "C" {
 
 size_t tlc_ckpt8_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols) {
     if (!valid_shape(rows, cols) || n < 1 || n > kMaxDim) return 0;
-    const Shape s = shape_of(rows, n, cols);
-    const uint64_t bytes = s.slices > 1 ? s.slices * n * cols * sizeof(float) : 0;
-    return std::max<size_t>((bytes + 255) / 256 * 256, 256);
+    uint64_t bytes = 256;
+    for (int terms = 1; terms <= 3; ++terms) {  // of any dtype
+        const Shape s = shape_of(rows, n, cols, terms);
+        if (s.slices > 1)
+            bytes = std::max<uint64_t>(bytes, s.slices * s.tiles_i * s.tiles_c * s.tile * s.tile * sizeof(float));
+    }
+    return bytes;
 }
 
 int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
@@ -413,8 +489,8 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
     if (rows && (!valid_matrix(dy, dtype, n, dy_stride) || !valid_checkpoint(codes, scales)))
         return TLC_ERR_INVALID_ARG;
     if (!valid_weight(col_scale, col_scale_dtype, dtype)) return TLC_ERR_INVALID_ARG;
-    const Shape s = shape_of(rows, n, cols);
-    if (s.tiles_i * s.tiles_c > (1u << 22)) return TLC_ERR_INVALID_ARG;
+    if (((n + 127) / 128) * ((cols + 127) / 128) > (1u << 24)) return TLC_ERR_INVALID_ARG;
+    const Shape s = shape_of(rows, n, cols, dtype == TLC_F32 ? 3 : dtype == TLC_F16 ? 2 : 1);
     if (!workspace || !aligned(workspace, 256) ||
         workspace_bytes < tlc_ckpt8_weight_grad_workspace_size(rows, n, cols))
         return TLC_ERR_WORKSPACE;
@@ -425,7 +501,7 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
     p.code_row = (uint32_t)code_stride(cols), p.scale_row = (uint32_t)scale_stride(cols);
     p.col_scale = col_scale;
     p.dw = dw, p.dw_stride = dw_stride, p.accumulate = accumulate != 0;
-    p.partial = s.slices > 1 ? static_cast<float*>(workspace) : nullptr;
+    p.partial = s.slices > 1 ? static_cast<f4*>(workspace) : nullptr;
     p.slice_rows = s.slice_rows;
     p.tiles = (uint32_t)(s.tiles_i * s.tiles_c);
     p.tiles_i = (uint32_t)s.tiles_i, p.tiles_c = (uint32_t)s.tiles_c;
@@ -436,18 +512,26 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
             return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
                 return with_format(format, [&](auto f) {
                     return launch("tlc_ckpt8_weight_grad", st, [&] {
-                        k_weight_grad<decltype(t), decltype(w), decltype(f)::value, 256><<<grid, kThreads, 0, st>>>(p);
+                        using T = decltype(t);
+                        using W = decltype(w);
+                        constexpr int F = decltype(f)::value;
+                        // 64 rows a step are faster in the small tile of one term (59 us instead of 69
+                        // for 4096x4096x1024 int8), slower with more LDS in use (1142 -> 1525 us, fp16)
+                        if (s.tile == 256)
+                            k_weight_grad<T, W, F, 256, 32><<<grid, kThreads, 0, st>>>(p);
+                        else
+                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32><<<grid, kThreads, 0, st>>>(p);
                     });
                 });
             });
         });
         if (rc || s.slices == 1) return rc;
     }
-    const uint32_t blocks = (uint32_t)std::min<uint64_t>(n * ((cols + kThreads - 1) / kThreads), 1u << 20);
+    const uint32_t blocks = p.tiles * (s.tile * s.tile / 4 / kThreads);
     return with_dtype(dtype, [&](auto t) {
         return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
             return launch("tlc_ckpt8_weight_sum", st, [&] {
-                k_weight_sum<decltype(w)><<<blocks, kThreads, 0, st>>>(p, s.slices);
+                k_weight_sum<decltype(w)><<<blocks, kThreads, 0, st>>>(p, s.slices, s.tile);
             });
         });
     });

@@ -526,7 +526,7 @@ int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, ui
  * optional: the weight of the norm whose unweighted checkpoint x is.  Products are exact (dy
  * as one, two or three bfloat16 numbers for bf16, fp16, fp32), sums fp32 in a
  * fixed order.  rows == 0: dw becomes 0, or stays with accumulate.
- * TLC_ERR_INVALID_ARG also for n and cols of more than 2^22 tiles of 256 x 256. */
+ * TLC_ERR_INVALID_ARG also for n and cols of more than 2^24 tiles of 128 x 128. */
 size_t tlc_ckpt8_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols);
 int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
                           const uint8_t* codes, const uint8_t* scales, uint64_t cols, const void* col_scale,
