@@ -125,20 +125,19 @@ __device__ __forceinline__ void places(const Walk& w, Place* at) {
 __device__ __forceinline__ void store_codes(uint8_t* codes, uint8_t* scales, const Walk& w, const Place& p, u2 c,
                                             uint32_t byte) {
     if (p.n < 0) return;
-    *reinterpret_cast<u2*>(codes + (p.row * w.per_row + p.unit) * 8) = c;
+    __builtin_nontemporal_store(c, reinterpret_cast<u2*>(codes + (p.row * w.per_row + p.unit) * 8));
     if ((p.unit & 3) == 0) scales[p.row * w.scale_row + p.unit / 4] = (uint8_t)byte;
     // the scales' own pads, at the end of the row
     if (p.unit == w.per_row - 1)
         for (uint32_t g = w.per_row / 4; g < w.scale_row; ++g) scales[p.row * w.scale_row + g] = 0;
 }
 
-template <int FMT>
 __device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, const Walk& w, const Place& p,
                                            u2* c, uint32_t* byte) {
     *c = u2{0, 0};
     *byte = 0;
     if (p.n <= 0) return;
-    *c = *reinterpret_cast<const u2*>(codes + (p.row * w.per_row + p.unit) * 8);
+    *c = __builtin_nontemporal_load(reinterpret_cast<const u2*>(codes + (p.row * w.per_row + p.unit) * 8));
     *byte = scales[p.row * w.scale_row + p.unit / 4];
 }
 
@@ -157,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void k_act(Walk w, const typename T::Elem
     Raw8<T> ra[U], rb[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        ra[i] = load8<T>(a + at[i].row * a_stride + at[i].unit * 8ull, at[i].n);
+        ra[i] = load8<T, kInputs == 0>(a + at[i].row * a_stride + at[i].unit * 8ull, at[i].n);
         if constexpr (kInputs == 2) rb[i] = load8<T>(b + at[i].row * b_stride + at[i].unit * 8ull, at[i].n);
     }
 #pragma unroll
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void k_unpack(Walk w, const uint8_t* __re
     u2 c[U];
     uint32_t byte[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) load_codes<FMT>(codes, scales, w, at[i], &c[i], &byte[i]);
+    for (int i = 0; i < U; ++i) load_codes(codes, scales, w, at[i], &c[i], &byte[i]);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         float v[8];
@@ -209,7 +208,8 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(
     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_scales, const typename T::Elem* dy,
     uint64_t dy_stride, typename T::Elem* da, uint64_t da_stride, typename T::Elem* db, uint64_t db_stride,
     uint8_t* __restrict__ y_codes, uint8_t* __restrict__ y_scales) {
-    constexpr int U = 2;
+    // two checkpoints are enough under way with one unit a lane (16384x8192: 208 -> 197 us)
+    constexpr int U = kGated ? 1 : 2;
     constexpr bool kPrecise = T::kTerms == 3;
     Place at[U];
     places<U>(w, at);
@@ -218,9 +218,9 @@ __global__ __launch_bounds__(kThreads) void k_act_grad(
     Raw8<T> rd[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        load_codes<FMT>(a_codes, a_scales, w, at[i], &ca[i], &ea[i]);
-        if constexpr (kGated) load_codes<FMT>(b_codes, b_scales, w, at[i], &cb[i], &eb[i]);
-        rd[i] = load8<T>(dy + at[i].row * dy_stride + at[i].unit * 8ull, at[i].n);
+        load_codes(a_codes, a_scales, w, at[i], &ca[i], &ea[i]);
+        if constexpr (kGated) load_codes(b_codes, b_scales, w, at[i], &cb[i], &eb[i]);
+        rd[i] = load8<T, true>(dy + at[i].row * dy_stride + at[i].unit * 8ull, at[i].n);
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
             }
             const u2 c = encode8_64<FMT>(d, (double)inverse_scale(byte), byte);
             if (live && unit < p.units) {
-                *reinterpret_cast<u2*>(p.codes + (row * p.units + unit) * 8) = c;
+                __builtin_nontemporal_store(c, reinterpret_cast<u2*>(p.codes + (row * p.units + unit) * 8));
                 if ((unit & 3) == 0) p.scales[row * p.scale_row + unit / 4] = (uint8_t)byte;
                 if (unit == p.units - 1)
                     for (uint32_t g = p.units / 4; g < p.scale_row; ++g) p.scales[row * p.scale_row + g] = 0;
@@ -425,12 +425,14 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
     }
 }
 
-// Gradient of the norm: with n the normalised row (from its checkpoint, or
+// Gradient of the norm (FMT 0: from the sum): with n the normalised row (from its checkpoint, or
 // sum*rstd) and g = dy*w,
 //   dx = dsum + rstd*(g - n*mean(g*n)),   dw = sum over rows of dy*n.
-// A block walks over rows block, block + grid, ...; a lane keeps the dw of its
-// columns in registers and writes them once, as one row of `partial`, which
-// k_norm_dw adds in order: the same bits every run, no atomics.
+// A block walks over rows block, block + grid, ..., the next row's values on
+// their way while one is worked on; a lane keeps the dw of its columns in
+// registers.  The block's rows of them are added through LDS and written once,
+// as one row of `partial`, which k_norm_dw adds in order: the same bits every
+// run, no atomics.
 struct NormGradArgs {
     const void *dy, *dsum, *sum;
     uint64_t dy_stride, dsum_stride, sum_stride;
@@ -439,7 +441,7 @@ struct NormGradArgs {
     const float* rstd;
     void* dx;
     uint64_t dx_stride;
-    float* partial;  // [partial rows][cols], or nullptr
+    float* partial;  // [blocks][cols], or nullptr
     uint64_t rows;
     uint32_t cols, units, scale_row;
     int waves;
@@ -449,14 +451,49 @@ template <typename T, typename W, int FMT, int kVec>
 __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs p) {
     using Elem = typename T::Elem;
     __shared__ float sm[2][16];
+    __shared__ float sdw[kThreads * 8];  // of 4 wavefronts with 8 columns a lane at a time
     const int wave = threadIdx.x >> 6, rows_here = max(1, (int)(blockDim.x >> 6) / p.waves);
     const uint32_t lane = (wave % p.waves) * 64 + (threadIdx.x & 63), lanes = p.waves * 64;
+    constexpr bool kCodes = FMT != 0;
+    struct Row {
+        Raw8<T> dy[kVec], add[kVec], sum[kCodes ? 1 : kVec];  // dy, dsum and the sum, or instead of it:
+        u2 codes[kCodes ? kVec : 1];
+        uint32_t byte[kCodes ? kVec : 1];
+        float rstd;
+    };
+    const auto count = [&](int i) {
+        const uint32_t unit = lane + i * lanes;
+        return unit < p.units ? min(max((int)p.cols - (int)unit * 8, 0), 8) : 0;
+    };
+    const auto load = [&](Row& r, uint64_t row) {
+        const bool live = row < p.rows;
+        r.rstd = live ? p.rstd[row] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const uint32_t unit = lane + i * lanes;
+            const int n = live ? count(i) : 0;
+            r.dy[i] = load8<T, true>(static_cast<const Elem*>(p.dy) + row * p.dy_stride + unit * 8ull, n);
+            r.add[i] = load8<T, true>(static_cast<const Elem*>(p.dsum) + row * p.dsum_stride + unit * 8ull,
+                                      p.dsum ? n : 0);
+            if constexpr (kCodes) {
+                r.codes[i] = u2{0, 0};
+                r.byte[i] = 0;
+                if (n > 0) {
+                    r.codes[i] =
+                        __builtin_nontemporal_load(reinterpret_cast<const u2*>(p.codes + (row * p.units + unit) * 8));
+                    r.byte[i] = p.scales[row * p.scale_row + unit / 4];
+                }
+            } else {
+                r.sum[i] = load8<T, true>(static_cast<const Elem*>(p.sum) + row * p.sum_stride + unit * 8ull, n);
+            }
+        }
+    };
     float w[kVec][8], dw[kVec][8];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const uint32_t unit = lane + i * lanes;
-        const int n = unit < p.units ? min(max((int)p.cols - (int)unit * 8, 0), 8) : 0;
-        if (p.weight) unpack8<W>(load8<W>(static_cast<const typename W::Elem*>(p.weight) + unit * 8ull, n), w[i]);
+        if (p.weight)
+            unpack8<W>(load8<W>(static_cast<const typename W::Elem*>(p.weight) + (lane + i * lanes) * 8ull, count(i)),
+                       w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (!p.weight) w[i][j] = 1.0f;
@@ -464,29 +501,30 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs p) {
         }
     }
     int turn = 0;
+    Row now, next;
+    const uint64_t stride = (uint64_t)gridDim.x * rows_here;
+    uint64_t base = (uint64_t)blockIdx.x * rows_here;
+    constexpr bool kAhead = kVec == 1;  // more would not fit the registers
+    if constexpr (kAhead) load(now, base + wave / p.waves);
     // every wavefront of a block makes the same turns: barriers lie inside
-    for (uint64_t base = (uint64_t)blockIdx.x * rows_here; base < p.rows; base += (uint64_t)gridDim.x * rows_here) {
+    for (; base < p.rows; base += stride) {
         const uint64_t row = base + wave / p.waves;
         const bool live = row < p.rows;
-        const float rstd = live ? p.rstd[row] : 0.0f;
+        if constexpr (kAhead)
+            load(next, row + stride);
+        else
+            load(now, row);
         float g[kVec][8], nv[kVec][8], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const uint32_t unit = lane + i * lanes;
-            const int n = live && unit < p.units ? min(max((int)p.cols - (int)unit * 8, 0), 8) : 0;
-            unpack8<T>(load8<T>(static_cast<const Elem*>(p.dy) + row * p.dy_stride + unit * 8ull, n), g[i]);
-            if (p.codes) {
-                u2 c = {0, 0};
-                uint32_t byte = 0;
-                if (n > 0) {
-                    c = *reinterpret_cast<const u2*>(p.codes + (row * p.units + unit) * 8);
-                    byte = p.scales[row * p.scale_row + unit / 4];
-                }
-                decode8<FMT>(c, byte, nv[i]);
+            const int n = count(i);
+            unpack8<T>(now.dy[i], g[i]);
+            if constexpr (kCodes) {
+                decode8<FMT>(now.codes[i], now.byte[i], nv[i]);
             } else {
-                unpack8<T>(load8<T>(static_cast<const Elem*>(p.sum) + row * p.sum_stride + unit * 8ull, n), nv[i]);
+                unpack8<T>(now.sum[i], nv[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) nv[i][j] *= rstd;
+                for (int j = 0; j < 8; ++j) nv[i][j] *= now.rstd;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -500,50 +538,68 @@ __global__ __launch_bounds__(1024) void k_norm_grad(NormGradArgs p) {
         const float mean = dot / (float)p.cols;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-            const uint32_t unit = lane + i * lanes;
-            const int n = live && unit < p.units ? min(max((int)p.cols - (int)unit * 8, 0), 8) : 0;
+            const int n = live ? count(i) : 0;
             float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = rstd * (g[i][j] - nv[i][j] * mean);
-            if (p.dsum) {
-                float d[8];
-                unpack8<T>(load8<T>(static_cast<const Elem*>(p.dsum) + row * p.dsum_stride + unit * 8ull, n), d);
+            for (int j = 0; j < 8; ++j) o[j] = now.rstd * (g[i][j] - nv[i][j] * mean);
+            float d[8];
+            unpack8<T>(now.add[i], d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += d[j];
-            }
-            if (n > 0) store8<T>(static_cast<Elem*>(p.dx) + row * p.dx_stride + unit * 8ull, n, pack8<T>(o));
+            for (int j = 0; j < 8; ++j) o[j] += d[j];
+            if (n > 0)
+                store8<T>(static_cast<Elem*>(p.dx) + row * p.dx_stride + (lane + i * lanes) * 8ull, n, pack8<T>(o));
         }
+        if constexpr (kAhead) now = next;
     }
     if (!p.partial) return;
-    float* const out = p.partial + ((uint64_t)blockIdx.x * rows_here + wave / p.waves) * p.cols;
+    float* const out = p.partial + (uint64_t)blockIdx.x * p.cols;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const uint32_t unit = lane + i * lanes;
-        const int n = unit < p.units ? min(max((int)p.cols - (int)unit * 8, 0), 8) : 0;
-        if (n > 0) store8<F32>(out + unit * 8ull, n, pack8<F32>(dw[i]));
+        if (rows_here > 1) {  // waves of 1 or 2: the block's rows add up, in order
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sdw[(j * rows_here + wave / p.waves) * lanes + lane] = dw[i][j];
+            __syncthreads();
+            if (wave / p.waves == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    for (int r = 1; r < rows_here; ++r) dw[i][j] += sdw[(j * rows_here + r) * lanes + lane];
+        }
+        const int n = count(i);
+        if (n > 0 && wave / p.waves == 0) store8<F32>(out + (lane + i * lanes) * 8ull, n, pack8<F32>(dw[i]));
     }
 }
 
-// dw[c] (+)= sum over the partial rows, in order: 8 strips of rows per block,
-// each added by one lane per column, then the strips.
-__global__ __launch_bounds__(kThreads) void k_norm_dw(const float* __restrict__ partial, uint32_t parts, uint32_t cols,
-                                                      float* dw, int accumulate) {
-    __shared__ float sm[8][32];
+// dw[c] (+)= sum over the partial rows, in order: 32 strips of rows per block,
+// each added by one lane per column with four loads under way, then the strips.
+constexpr int kStrips = 32;
+__global__ __launch_bounds__(32 * kStrips) void k_norm_dw(const float* __restrict__ partial, uint32_t parts,
+                                                          uint32_t cols, float* dw, int accumulate) {
+    __shared__ float sm[kStrips][32];
     const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31), strip = threadIdx.x >> 5;
     float s = 0.0f;
-    if (c < cols)
-        for (uint32_t r = strip; r < parts; r += 8) s += partial[(uint64_t)r * cols + c];
+    if (c < cols) {
+        uint32_t r = strip;
+        for (; r + 3 * kStrips < parts; r += 4 * kStrips) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = partial[(uint64_t)(r + k * kStrips) * cols + c];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s += v[k];
+        }
+        for (; r < parts; r += kStrips) s += partial[(uint64_t)r * cols + c];
+    }
     sm[strip][threadIdx.x & 31] = s;
     __syncthreads();
     if (strip || c >= cols) return;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sm[k][threadIdx.x & 31];
+    for (int k = 1; k < kStrips; ++k) s += sm[k][threadIdx.x & 31];
     dw[c] = accumulate ? dw[c] + s : s;
 }
 
 // ---- host ------------------------------------------------------------------
 
-constexpr uint64_t kNormMaxCols = 32768;  // 16 wavefronts of 4 units a lane
+constexpr uint64_t kNormMaxCols = 16384;  // 16 wavefronts of 2 units a lane
 
 struct NormShape {
     int waves, vec, threads;
@@ -552,22 +608,29 @@ struct NormShape {
 NormShape norm_shape(uint64_t cols) {
     const uint64_t units = 4 * groups_of(cols);
     NormShape s;
+    // a unit a lane up to 8192 columns, two past them
+    s.vec = units <= 16 * 64 ? 1 : 2;
     s.waves = 1;
-    while (s.waves < 16 && (uint64_t)s.waves * 64 < units) s.waves *= 2;
-    s.vec = 1;
-    while ((uint64_t)s.waves * 64 * s.vec < units) s.vec *= 2;
+    while ((uint64_t)s.waves * 64 * s.vec < units) s.waves *= 2;
     s.threads = std::max(kThreads, s.waves * 64);
     s.rows_here = (uint32_t)(s.threads / 64 / s.waves);
     return s;
 }
+// Blocks of the gradient: two rows a wavefront at least, so that the partial
+// sums stay below what they sum.
 constexpr uint64_t kNormGradBlocks = 512;
 uint64_t norm_grad_blocks(uint64_t rows, const NormShape& s) {
-    return std::min<uint64_t>((rows + s.rows_here - 1) / s.rows_here, kNormGradBlocks);
+    return std::min<uint64_t>((rows + 2 * s.rows_here - 1) / (2 * s.rows_here), kNormGradBlocks);
 }
 
 template <typename Fn>
 int with_vec(int vec, Fn&& fn) {
-    return vec == 1 ? fn(Int<1>{}) : vec == 2 ? fn(Int<2>{}) : fn(Int<4>{});
+    return vec == 1 ? fn(Int<1>{}) : fn(Int<2>{});
+}
+
+template <typename Fn>
+int with_saved(int format, Fn&& fn) {
+    return format ? with_format(format, fn) : fn(Int<0>{});
 }
 
 // Blocks of a walk with U units a lane; 0: too many for one launch.
@@ -681,7 +744,7 @@ int tlc_ckpt8_act_grad(int act, const uint8_t* a_codes, const uint8_t* a_scales,
         return TLC_ERR_INVALID_ARG;
     if ((y_codes || y_scales) && !valid_checkpoint(y_codes, y_scales)) return TLC_ERR_INVALID_ARG;
     const Walk w = walk_of(rows, cols);
-    const uint32_t blocks = walk_blocks(w, kThreads * 2);
+    const uint32_t blocks = walk_blocks(w, kThreads * (gated ? 1 : 2));
     if (!blocks) return TLC_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
@@ -748,7 +811,7 @@ int tlc_ckpt8_norm(const void* x, uint64_t x_stride, const void* residual, uint6
 size_t tlc_ckpt8_norm_grad_workspace_size(uint64_t rows, uint64_t cols) {
     if (!valid_shape(rows, cols) || cols > kNormMaxCols) return 0;
     const NormShape s = norm_shape(cols);
-    return std::max<size_t>((norm_grad_blocks(rows, s) * s.rows_here * cols * sizeof(float) + 255) / 256 * 256, 256);
+    return std::max<size_t>((norm_grad_blocks(rows, s) * cols * sizeof(float) + 255) / 256 * 256, 256);
 }
 
 int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, uint64_t dsum_stride, int dtype,
@@ -787,7 +850,7 @@ int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, ui
         p.scale_row = (uint32_t)scale_stride(cols), p.waves = s.waves;
         const int rc = with_dtype(dtype, [&](auto t) {
             return with_weight(t, weight, weight_dtype, [&](auto w) {
-                return with_format(codes ? format : TLC_CKPT8_INT8, [&](auto f) {
+                return with_saved(codes ? format : 0, [&](auto f) {
                     return with_vec(s.vec, [&](auto v) {
                         return launch("tlc_ckpt8_norm_grad", st, [&] {
                             k_norm_grad<decltype(t), decltype(w), decltype(f)::value, decltype(v)::value>
@@ -801,8 +864,8 @@ int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, ui
     }
     if (!dw || (!rows && accumulate)) return TLC_OK;
     return launch("tlc_ckpt8_norm_dw", st, [&] {
-        k_norm_dw<<<(uint32_t)((cols + 31) / 32), kThreads, 0, st>>>(partial, blocks * s.rows_here, (uint32_t)cols, dw,
-                                                                     accumulate != 0);
+        k_norm_dw<<<(uint32_t)((cols + 31) / 32), 32 * kStrips, 0, st>>>(partial, blocks, (uint32_t)cols, dw,
+                                                                         accumulate != 0);
     });
 }
 

@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(
 #pragma unroll
             for (int q = 1; q + 1 < kRounds; ++q) round(now, q);
         }
-        if constexpr (kMain) interleave<kTiles * kTiles * (kRounds - 1)>();
+        if constexpr (kMain && kTerms == 1) interleave<kTiles * kTiles * (kRounds - 1)>();
         __syncthreads();
         b8v last_a[kTiles], last_b[kTiles];
 #pragma unroll

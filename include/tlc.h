@@ -495,7 +495,7 @@ int tlc_ckpt8_act_grad(int act, const uint8_t* a_codes, const uint8_t* a_scales,
  *   codes, scales: the checkpoint of n (weighted 0: what the gradients below
  *          take) or of n*weight (weighted 1: an 8-bit input for the next
  *          product), from n in 64 bits; given together or not at all.
- * One of y and codes at least.  cols <= 32768; eps > 0 and finite.  The squares
+ * One of y and codes at least.  cols <= 16384; eps > 0 and finite.  The squares
  * are summed in 64 bits. */
 int tlc_ckpt8_norm(const void* x, uint64_t x_stride, const void* residual, uint64_t residual_stride, int dtype,
                    uint64_t rows, uint64_t cols, const void* weight, int weight_dtype, float eps, int weighted,

@@ -29,7 +29,7 @@ int main() {
         const size_t w = tlc_ckpt8_weight_grad_workspace_size(rows, n, cols);
         CHECK(w % 256 == 0 && (w > 0) == (rows <= top && n <= top && cols <= top));
         const size_t g = tlc_ckpt8_norm_grad_workspace_size(rows, cols);
-        CHECK(g % 256 == 0 && (g > 0) == (rows <= top && cols <= 32768));
+        CHECK(g % 256 == 0 && (g > 0) == (rows <= top && cols <= 16384));
     }
     void* const p = reinterpret_cast<void*>(0x10000);
     uint8_t* const b = static_cast<uint8_t*>(p);
@@ -43,7 +43,7 @@ int main() {
     CHECK(tlc_ckpt8_act(9, p, 64, p, 64, 2, 4, 40, p, 64, 1, b, b, b, b, nullptr) == bad);
     CHECK(tlc_ckpt8_act(1, p, 64, nullptr, 0, 2, 4, 40, p, 64, 1, b, b, b, b, nullptr) == bad);
     CHECK(tlc_ckpt8_act_grad(1, b, b, b, nullptr, 1, p, 64, 2, 4, 40, p, 64, p, 64, b, b, nullptr) == bad);
-    CHECK(tlc_ckpt8_norm(p, 64, p, 64, 2, 4, 32769, p, 2, 1e-5f, 0, p, 64, p, 64, 1, b, b, f, nullptr) == bad);
+    CHECK(tlc_ckpt8_norm(p, 64, p, 64, 2, 4, 16385, p, 2, 1e-5f, 0, p, 64, p, 64, 1, b, b, f, nullptr) == bad);
     CHECK(tlc_ckpt8_norm(p, 64, p, 64, 2, 4, 40, p, 1, 1e-5f, 0, p, 64, p, 64, 1, b, b, f, nullptr) == bad);
     CHECK(tlc_ckpt8_norm_grad(p, 64, p, 64, 2, ~0ull, 40, nullptr, 0, 1, b, b, f, p, 2, p, 64, f, 0, p, 1u << 30,
                               nullptr) == bad);

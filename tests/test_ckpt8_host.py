@@ -33,13 +33,13 @@ def test_strides():
 
 def test_workspace_sizes():
     assert tlc.ckpt8_norm_grad_workspace_size(10, 0) == 0
-    assert tlc.ckpt8_norm_grad_workspace_size(10, 32769) == 0
+    assert tlc.ckpt8_norm_grad_workspace_size(10, 16385) == 0
     assert tlc.ckpt8_norm_grad_workspace_size(BIG, 64) == 0
     assert tlc.ckpt8_weight_grad_workspace_size(10, 0, 64) == 0
     assert tlc.ckpt8_weight_grad_workspace_size(10, 64, 0) == 0
     assert tlc.ckpt8_weight_grad_workspace_size(BIG, 64, 64) == 0
     for rows in (0, 1, 100, 1 << 20):
-        for cols in (1, 33, 1024, 32768):
+        for cols in (1, 33, 1024, 16384):
             v = tlc.ckpt8_norm_grad_workspace_size(rows, cols)
             assert v >= 256 and v % 256 == 0
             # a row of fp32 sums per wavefront at most, of a bounded number of blocks
@@ -92,7 +92,7 @@ def test_norm_refusals():
     #       x  xs  r  rs  dt r  c   w  wd eps  wtd s  ss  y  ys  fmt c  s  rstd
     good = [P, 64, P, 64, 2, 4, 40, P, 2, 1e-5, 0, P, 64, P, 64, 1, P, P, P, None]
     nan, inf = float("nan"), float("inf")
-    for at, v in [(0, None), (0, ODD), (1, 39), (2, ODD), (3, 39), (4, 3), (5, BIG), (6, 0), (6, 32769), (7, ODD),
+    for at, v in [(0, None), (0, ODD), (1, 39), (2, ODD), (3, 39), (4, 3), (5, BIG), (6, 0), (6, 16385), (7, ODD),
                   (8, 3), (8, 1), (9, 0.0), (9, -1.0), (9, nan), (9, inf), (11, ODD), (12, 39), (13, ODD), (14, 39), (15, 0),
                   (16, None), (16, FOUR), (17, None), (18, TWO), (2, None)]:
         a = list(good)
@@ -107,7 +107,7 @@ def test_norm_refusals():
     f = L().tlc_ckpt8_norm_grad
     #       dy ds  dt  dts dtype r c  sum ss fmt c  s  rstd w  wd dx dxs dw acc ws  nws
     good = [P, 64, P, 64, 2, 4, 40, None, 0, 1, P, P, P, P, 2, P, 64, P, 0, P, 1 << 20, None]
-    for at, v in [(0, None), (1, 39), (2, ODD), (3, 39), (4, 3), (5, BIG), (6, 0), (6, 32769), (7, P), (9, 0),
+    for at, v in [(0, None), (1, 39), (2, ODD), (3, 39), (4, 3), (5, BIG), (6, 0), (6, 16385), (7, P), (9, 0),
                   (10, None), (11, None), (12, None), (12, TWO), (13, ODD), (14, 3), (14, 1), (15, None), (16, 39), (17, TWO)]:
         a = list(good)
         a[at] = v
