@@ -840,19 +840,41 @@ def _checkpoint(c: Checkpoint8, name: str, rows: int, cols: int, device):
     return c.codes.data_ptr(), c.scales.data_ptr()
 
 
-def _new_checkpoint(rows: int, cols: int, fmt: int, device) -> Checkpoint8:
+def _checkpoint_for(out: Checkpoint8 | None, name: str, rows: int, cols: int, fmt: int, device):
+    """(checkpoint, codes pointer, scales pointer): `out`, checked, or a new one."""
+    if out is not None:
+        if out.format != fmt:
+            raise ValueError(f"{name} is of another format")
+        return (out, *_checkpoint(out, name, rows, cols, device))
     groups = -(-cols // 32)
-    return Checkpoint8(torch.empty((rows, 32 * groups), dtype=torch.uint8, device=device),
-                       torch.empty((rows, -(-groups // 4) * 4), dtype=torch.uint8, device=device), cols, fmt)
+    codes = torch.empty((rows, 32 * groups), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, -(-groups // 4) * 4), dtype=torch.uint8, device=device)
+    return Checkpoint8(codes, scales, cols, fmt), codes.data_ptr(), scales.data_ptr()
+
+
+def _matrix_for(out: torch.Tensor | None, name: str, like: torch.Tensor):
+    """(matrix, pointer, row stride): `out`, checked, or a new one of like's shape and dtype."""
+    if out is not None:
+        return (out, *_matrix(out, name, like))
+    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return out, out.data_ptr(), like.shape[1]
+
+
+def _current_stream_handle(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle alone, without a Stream object around it (0.1 instead of 2.7 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_handle)
 
 
 def _on_stream(device, stream, body):
     """body(stream handle) with `device` and `stream` (or the device's current one) current."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_raw_stream(device.index))
         with torch.cuda.device(device):
-            return body(torch.cuda.current_stream().cuda_stream)
+            return body(_raw_stream(device.index))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
@@ -875,10 +897,7 @@ def ckpt8_pack(x: torch.Tensor, fmt: int, *, out: Checkpoint8 | None = None, str
     rows, cols = x.shape
 
     def body(st):
-        c = out if out is not None else _new_checkpoint(rows, cols, fmt, x.device)
-        pc, ps = _checkpoint(c, "out", rows, cols, x.device)
-        if c.format != fmt:
-            raise ValueError("out is of another format")
+        c, pc, ps = _checkpoint_for(out, "out", rows, cols, fmt, x.device)
         _check(lib().tlc_ckpt8_pack(px, sx, _DTYPES[x.dtype], rows, cols, fmt, pc, ps, st), "tlc_ckpt8_pack")
         return c
     return _on_stream(x.device, stream, body)
@@ -889,12 +908,18 @@ def ckpt8_unpack(c: Checkpoint8, dtype: torch.dtype = torch.bfloat16, *, y: torc
     """The values a checkpoint stands for (exact in float32 and bfloat16)."""
     rows, cols, device = c.rows, c.cols, c.codes.device
     pc, ps = _checkpoint(c, "checkpoint", rows, cols, device)
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
 
     def body(st):
-        o = y if y is not None else torch.empty((rows, cols), dtype=dtype, device=device)
-        po, so = _matrix(o, "y")
-        if o.shape[0] != rows or o.shape[1] != cols or o.device != device:
-            raise ValueError(f"y must be ({rows}, {cols}) on {device}")
+        if y is None:
+            o = torch.empty((rows, cols), dtype=dtype, device=device)
+            po, so = o.data_ptr(), cols
+        else:
+            o = y
+            po, so = _matrix(o, "y")
+            if o.shape[0] != rows or o.shape[1] != cols or o.device != device:
+                raise ValueError(f"y must be ({rows}, {cols}) on {device}")
         _check(lib().tlc_ckpt8_unpack(pc, ps, c.format, rows, cols, po, so, _DTYPES[o.dtype], st),
                "tlc_ckpt8_unpack")
         return o
@@ -914,14 +939,11 @@ def ckpt8_act(a: torch.Tensor, act: int, fmt: int, b: torch.Tensor | None = None
         raise ValueError("b_out needs b")
 
     def body(st):
-        o = y if y is not None else torch.empty((rows, cols), dtype=a.dtype, device=device)
-        po, so = _matrix(o, "y", a)
-        ca = a_out if a_out is not None else _new_checkpoint(rows, cols, fmt, device)
-        cb = None if b is None else b_out if b_out is not None else _new_checkpoint(rows, cols, fmt, device)
-        pca, psa = _checkpoint(ca, "a_out", rows, cols, device)
-        pcb, psb = _checkpoint(cb, "b_out", rows, cols, device) if cb is not None else (None, None)
-        if ca.format != fmt or cb is not None and cb.format != fmt:
-            raise ValueError("an output checkpoint is of another format")
+        o, po, so = _matrix_for(y, "y", a)
+        ca, pca, psa = _checkpoint_for(a_out, "a_out", rows, cols, fmt, device)
+        cb, pcb, psb = None, None, None
+        if b is not None:
+            cb, pcb, psb = _checkpoint_for(b_out, "b_out", rows, cols, fmt, device)
         _check(lib().tlc_ckpt8_act(act, pa, sa, pb, sb, _DTYPES[a.dtype], rows, cols, po, so, fmt, pca, psa, pcb,
                                    psb, st), "tlc_ckpt8_act")
         return o, ca, cb
@@ -944,19 +966,11 @@ def ckpt8_act_grad(dy: torch.Tensor, act: int, a: Checkpoint8, b: Checkpoint8 | 
         raise ValueError("db needs b")
 
     def body(st):
-        oa = da if da is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
-        poa, soa = _matrix(oa, "da", dy)
-        ob, pob, sob = None, None, 0
-        if b is not None:
-            ob = db if db is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
-            pob, sob = _matrix(ob, "db", dy)
-        cy, pcy, psy = y_out, None, None
-        if cy is None and want_y:
-            cy = _new_checkpoint(rows, cols, a.format, device)
-        if cy is not None:
-            pcy, psy = _checkpoint(cy, "y_out", rows, cols, device)
-            if cy.format != a.format:
-                raise ValueError("y_out is of another format")
+        oa, poa, soa = _matrix_for(da, "da", dy)
+        ob, pob, sob = _matrix_for(db, "db", dy) if b is not None else (None, None, 0)
+        cy, pcy, psy = None, None, None
+        if want_y or y_out is not None:
+            cy, pcy, psy = _checkpoint_for(y_out, "y_out", rows, cols, a.format, device)
         _check(lib().tlc_ckpt8_act_grad(act, pca, psa, pcb, psb, a.format, pd, sd, _DTYPES[dy.dtype], rows, cols, poa,
                                         soa, pob, sob, pcy, psy, st), "tlc_ckpt8_act_grad")
         return oa, ob, cy
@@ -984,21 +998,9 @@ def ckpt8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, fmt: in
         raise ValueError("total needs residual: without one the sum is x")
 
     def body(st):
-        t, pt, stt = x, None, 0
-        if residual is not None:
-            t = total if total is not None else torch.empty((rows, cols), dtype=x.dtype, device=device)
-            pt, stt = _matrix(t, "total", x)
-        o, po, so = y, None, 0
-        if o is None and want_y:
-            o = torch.empty((rows, cols), dtype=x.dtype, device=device)
-        if o is not None:
-            po, so = _matrix(o, "y", x)
-        c, pc, ps = None, None, None
-        if fmt is not None:
-            c = out if out is not None else _new_checkpoint(rows, cols, fmt, device)
-            pc, ps = _checkpoint(c, "out", rows, cols, device)
-            if c.format != fmt:
-                raise ValueError("out is of another format")
+        t, pt, stt = _matrix_for(total, "total", x) if residual is not None else (x, None, 0)
+        o, po, so = _matrix_for(y, "y", x) if want_y or y is not None else (None, None, 0)
+        c, pc, ps = _checkpoint_for(out, "out", rows, cols, fmt, device) if fmt is not None else (None, None, None)
         r = rstd if rstd is not None else torch.empty(rows, dtype=torch.float32, device=device)
         _check(lib().tlc_ckpt8_norm(px, sx, pr, sr, _DTYPES[x.dtype], rows, cols, pw, wdt, eps, int(weighted), pt, stt,
                                     po, so, fmt or 0, pc, ps, _vector(r, rows, device, "rstd", torch.float32)[0], st),
@@ -1037,8 +1039,7 @@ def ckpt8_norm_grad(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torch.T
         raise ValueError("accumulate needs dw")
 
     def body(st):
-        o = dx if dx is not None else torch.empty((rows, cols), dtype=dy.dtype, device=device)
-        po, so = _matrix(o, "dx", dy)
+        o, po, so = _matrix_for(dx, "dx", dy)
         g = dw
         if g is None and want_dw:
             g = torch.empty(cols, dtype=torch.float32, device=device)
