@@ -185,7 +185,7 @@ template <typename T, int FMT>
 __global__ __launch_bounds__(kThreads) void k_unpack(Walk w, const uint8_t* __restrict__ codes,
                                                      const uint8_t* __restrict__ scales,
                                                      typename T::Elem* __restrict__ y, uint64_t y_stride) {
-    constexpr int U = 4;
+    constexpr int U = 2;  // 32768x4096 to bf16: 66 us, 68 with four, 72 with eight
     Place at[U];
     places<U>(w, at);
     u2 c[U];
@@ -293,10 +293,11 @@ __device__ __forceinline__ S row_sum(S v, int waves, S* sm) {
 // after 21 bits with its last bit set if anything was cut off, which the
 // second rounding (to 4 bits) cannot take for a tie.
 __device__ __forceinline__ float cut_odd(double v) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t hi = (uint32_t)(u >> 32), mag = hi & 0x7FFFFFFFu;
-    const uint32_t odd = (mag << 3 | (uint32_t)((uint32_t)u != 0)) - (896u << 23);
-    return from_bits((mag >= 0x38100000u ? odd : 0u) | (hi & 0x80000000u));
+    // below 2^-20 every code is 0; the bound keeps the exponent in fp32's range
+    const uint64_t u = __builtin_bit_cast(uint64_t, fmax(fabs(v), 0x1p-20));
+    const uint32_t sign = (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32) & 0x80000000u;
+    const uint32_t mag = ((uint32_t)(u >> 32) << 3 | (uint32_t)((uint32_t)u != 0)) - (896u << 23);
+    return from_bits(mag | sign);
 }
 
 template <int FMT>
@@ -369,7 +370,8 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
     }
     ss = row_sum(ss, p.waves, sm);
     const double rstd = 1.0 / sqrt(ss / (double)p.cols + p.eps);
-    if (p.rstd && live && lane == 0) p.rstd[row] = (float)rstd;
+    const float rstd32 = (float)rstd;
+    if (p.rstd && live && lane == 0) p.rstd[row] = rstd32;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const uint32_t unit = lane + i * lanes;
@@ -417,7 +419,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
             float o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j] = (float)((double)v[i][j] * rstd);
+                o[j] = v[i][j] * rstd32;
                 if (p.weight) o[j] *= w[j];
             }
             store8<T>(static_cast<Elem*>(p.y) + row * p.y_stride + unit * 8ull, n, pack8<T>(o));
@@ -707,7 +709,7 @@ int tlc_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int format, ui
     if (rows == 0) return TLC_OK;
     if (!valid_matrix(y, dtype, cols, y_stride) || !valid_checkpoint(codes, scales)) return TLC_ERR_INVALID_ARG;
     const Walk w = walk_of(rows, cols);
-    const uint32_t blocks = walk_blocks(w, kThreads * 4);
+    const uint32_t blocks = walk_blocks(w, kThreads * 2);
     if (!blocks) return TLC_ERR_INVALID_ARG;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
