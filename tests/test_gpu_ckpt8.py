@@ -481,6 +481,84 @@ def test_weight_gradient(tlc, fmt, dtype):
         assert torch.equal(tlc.ckpt8_weight_grad(dy.cuda(), c), tlc.ckpt8_weight_grad(dy.cuda(), c))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_weight_gradient_of_many_tiles_is_exact(tlc, fmt, dtype):
+    """Sizes that take the larger tile, alone and in slices, with and without ragged edges; whole numbers, so that
+    every sum has one right value (below 2^24)."""
+    for k, (rows, n, cols) in enumerate([(300, 4000, 4100), (2000, 2100, 2000), (330, 4096, 4096), (700, 2048, 2048)]):
+        say(f"case weight_grad many tiles {rows}x{n}x{cols} {dtype} format {fmt}")
+        g = torch.Generator(device="cuda").manual_seed(k)
+        dy = torch.randint(-9, 10, (rows, n + 5), generator=g, device="cuda").to(dtype)[:, 3:n + 3]
+        x = torch.randint(-7, 8, (rows, cols), generator=g, device="cuda").float()
+        c = tlc.ckpt8_pack(x, fmt)
+        x = tlc.ckpt8_unpack(c, torch.float32).double()
+        want = dy.double().t().contiguous() @ x
+        assert torch.equal(tlc.ckpt8_weight_grad(dy, c).double(), want)
+        scale = torch.tensor([0.5, 1.0, 2.0, -1.0], device="cuda").repeat(-(-cols // 4))[:cols]
+        dw = torch.ones(n, cols + 1, device="cuda")[:, :cols]
+        tlc.ckpt8_weight_grad(dy, c, col_scale=scale.to((torch.float32, dtype)[k % 2]), dw=dw, accumulate=True)
+        assert torch.equal(dw.double(), want * scale.double() + 1)
+
+
+def test_norm_of_wide_rows_in_every_variant(tlc):
+    """Past 8192 columns, every type with either type of weight and either format."""
+    rows, cols = 3, 9001
+    for dtype in DTYPES:
+        for wt in {torch.float32, dtype}:
+            for fmt in FORMATS:
+                g = gen(5)
+                x, dy = randn(g, rows, cols, dtype=dtype, scale=2.0), randn(g, rows, cols, dtype=dtype)
+                w = (1 + randn(g, cols, scale=0.3)).to(wt)
+                _, y, c, rstd = tlc.ckpt8_norm(x.cuda(), w.cuda(), 1e-5, fmt)
+                r64, n = ref.norm(x.double(), float(torch.tensor(1e-5)))
+                assert_ck(c, *ref.encode(n, fmt), (dtype, wt, fmt))
+                want = n * w.double()
+                assert_close(y, want, want.abs() * (U[dtype] + 3 * 2.0 ** -24) * 1.01 + LEAST[dtype], "y")
+                for saved, nv in ((c, ref.decode(c.codes.cpu(), c.scales.cpu(), fmt, cols)), (x.cuda(), None)):
+                    r = rstd.cpu().double()
+                    nv = x.double() * r.unsqueeze(1) if nv is None else nv
+                    dx, dw = tlc.ckpt8_norm_grad(dy.cuda(), saved, rstd, w.cuda())
+                    want, want_dw = ref.norm_grad(dy.double(), nv, r, w.double())
+                    gn = (dy.double() * w.double()).abs()
+                    part = r.unsqueeze(1) * (gn + nv.abs() * (gn * nv.abs()).mean(1, keepdim=True))
+                    assert_close(dx, want, U[dtype] * want.abs() * 1.01 + (6 + cols / 64) * 2.0 ** -24 * part
+                                 + LEAST[dtype], "dx")
+                    assert_close(dw, want_dw, (rows + 4) * 2.0 ** -24 * (dy.double() * nv).abs().sum(0) + 2.0 ** -149,
+                                 "dw")
+
+
+def test_offsets_past_32_bits(tlc):
+    """More than 2^32 values: the last rows of the whole are what they are alone."""
+    rows, cols, last = 1_100_000, 4096, 300
+    say(f"case offsets {rows}x{cols}")
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[-last:] = torch.randint(-7, 8, (last, cols), generator=g, device="cuda").to(torch.bfloat16)
+    for fmt in FORMATS:
+        c, alone = tlc.ckpt8_pack(x, fmt), tlc.ckpt8_pack(x[-last:], fmt)
+        assert torch.equal(c.codes[-last:], alone.codes) and torch.equal(c.scales[-last:], alone.scales)
+        y = tlc.ckpt8_unpack(c)
+        assert torch.equal(y[-last:], x[-last:]) and torch.equal(y[:last], x[:last])
+        del y
+    da = tlc.ckpt8_act_grad(x, ref.SILU, c)[0]
+    assert torch.equal(da[-last:], tlc.ckpt8_act_grad(x[-last:], ref.SILU, alone)[0])
+    del da
+    _, y, n8, rstd = tlc.ckpt8_norm(x, None, 1e-5, ref.INT8)
+    _, y_alone, n8_alone, rstd_alone = tlc.ckpt8_norm(x[-last:], None, 1e-5, ref.INT8)
+    assert torch.equal(y[-last:], y_alone) and torch.equal(n8.codes[-last:], n8_alone.codes)
+    assert torch.equal(rstd[-last:], rstd_alone)
+    dx, _ = tlc.ckpt8_norm_grad(x, n8, rstd)
+    assert torch.equal(dx[-last:], tlc.ckpt8_norm_grad(x[-last:], n8_alone, rstd_alone)[0])
+    del y, dx, n8
+    # a gradient that is 0 but in the last rows: the sums are those rows' alone
+    dy = torch.zeros(rows, 16, dtype=torch.bfloat16, device="cuda")
+    dy[-last:] = torch.randint(-9, 10, (last, 16), generator=g, device="cuda").to(torch.bfloat16)
+    want = dy[-last:].double().t().contiguous() @ x[-last:].double()
+    assert torch.equal(tlc.ckpt8_weight_grad(dy, c).double(), want)
+
+
 def test_weight_gradient_of_no_rows(tlc):
     for dtype in DTYPES:
         c = tlc.Checkpoint8(torch.empty(0, 64, dtype=torch.uint8, device="cuda"),
