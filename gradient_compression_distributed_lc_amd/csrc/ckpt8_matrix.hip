@@ -15,7 +15,7 @@ namespace {
 using namespace tlc_ckpt8;
 using tlc_internal::launch;
 
-constexpr int kThreads = 256;  // four wavefronts, two by two
+constexpr int kThreads = 256;  // of a group: four wavefronts, two by two
 
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
@@ -86,8 +86,12 @@ __device__ __forceinline__ float column_scale(const void* p, uint32_t c) {
     return (float)static_cast<const typename W::Elem*>(p)[c];
 }
 
-// The product.  A block computes kTile x kTile values of dw, each wavefront a
-// quarter, as 32x32x16 products.  Both operands lie with the reduction (the
+// The product.  A block computes kTile x kTile values of dw, each wavefront of a
+// group a quarter, as 32x32x16 products.  With two groups each takes half of
+// the rows in stages of its own, and their sums are added at the end: two
+// wavefronts a SIMD cover each other's waits, which the small tile needs (its
+// wavefronts have half the products per operand read; 4096x4096x1024 54 -> 43
+// us).  The large tile's sums leave registers for one only.  Both operands lie with the reduction (the
 // rows t) as the slow index, in memory and, unchanged, in LDS: [t][column].
 // The transposing LDS read turns them: 16 lanes read 4 rows of 16 columns and
 // each gets 4 rows of one column.  Which 8 of the 16 rows a lane holds is the
@@ -137,8 +141,8 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <typename T, typename W, int FMT, int kTile, int kStep>
-__global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(MatArgs p) {
+template <typename T, typename W, int FMT, int kTile, int kStep, int kGroups>
+__global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p) {
     using Elem = typename T::Elem;
     constexpr int kTerms = T::kTerms;
     constexpr int kWave = kTile / 2, kTiles = kWave / 32;
@@ -147,7 +151,10 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(
     constexpr int kLoadsB = kStep * kTile / 16 / kThreads;     // 16-byte units of codes a lane
     static_assert(kLoadsA >= 1 && kLoadsB >= 1, "too narrow a tile");
     using Buffer = Stage<kTerms, kTile, kStep>;
-    __shared__ Buffer stage0, stage1;
+    __shared__ Buffer stages0[kGroups], stages1[kGroups];
+    const int tid = threadIdx.x % kThreads;
+    const int group = kGroups == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / kThreads);
+    Buffer &stage0 = stages0[group], &stage1 = stages1[group];
 
     // neighbouring tiles on one XCD: blocks go round the 8 of them
     uint32_t b = blockIdx.x;
@@ -157,14 +164,17 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(
     uint32_t tile_i, tile_c;
     tile_place(p, tile, &tile_i, &tile_c);
     const uint32_t i0 = tile_i * kTile, c0 = tile_c * kTile;
-    const uint64_t t_begin = slice * p.slice_rows, t_end = min(p.rows, t_begin + p.slice_rows);
-    const int steps = (int)((t_end - t_begin + kStep - 1) / kStep);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // the group's share of the slice's rows, the same steps for each group
+    const uint64_t s_begin = slice * p.slice_rows, s_end = min(p.rows, s_begin + p.slice_rows);
+    const uint64_t share = ((s_end - s_begin + kGroups - 1) / kGroups + kStep - 1) / kStep * kStep;
+    const uint64_t t_begin = min(s_begin + group * share, s_end), t_end = min(t_begin + share, s_end);
+    const int steps = (int)(share / kStep);
+    const int wave = tid >> 6, lane = tid & 63;
 
     // what the lane loads: rows ra + i*(rows between), columns from i0 + 8*ua; codes likewise
-    const int ra = threadIdx.x / kUnits, ua = threadIdx.x % kUnits;
+    const int ra = tid / kUnits, ua = tid % kUnits;
     // (codes: 4 neighbouring units of two rows in 8 lanes)
-    const int pair = threadIdx.x / (kTile / 8), in_pair = threadIdx.x % (kTile / 8);
+    const int pair = tid / (kTile / 8), in_pair = tid % (kTile / 8);
     const int rb = 2 * pair + (in_pair >> 2 & 1), ub = (in_pair & 3) | in_pair >> 3 << 2;
     constexpr int kRowsA = kThreads / kUnits, kRowsB = kThreads / (kTile / 16);
     // A lane past the last column loads the row's first ones, and a unit that
@@ -345,57 +355,82 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_weight_grad(
         if (s + 1 < steps) step(stage1, stage0, g1, g0, s + 1, Int<0>{});
     }
 
-    // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32
-    if (p.partial) {  // four rows a store, each lane's registers side by side: the sum's business to sort out
-        f4* const out = p.partial + (uint64_t)b * (kTile * kTile / 4) + wave * (kTile * kTile / 16) + lane;
+    // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32.
+    // One row of the wavefront's 32x32 parts to where it belongs:
+    const uint32_t col0 = c0 + wc + (lane & 31);
+    float cs[kTiles];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+    for (int c = 0; c < kTiles; ++c) cs[c] = column_scale<W>(p.col_scale, min(col0 + c * 32, p.cols - 1));
+    const bool direct = i0 + kTile <= p.n && c0 + kTile <= p.cols && !p.accumulate;
+    auto write = [&](int i, const f16v* v) {
+        if (p.partial) {  // four rows a store, each lane's registers side by side: the sum's business to sort out
+            f4* const out = p.partial + (uint64_t)b * (kTile * kTile / 4) + wave * (kTile * kTile / 16) + lane;
 #pragma unroll
             for (int c = 0; c < kTiles; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    out[((i * kTiles + c) * 4 + j) * 64] = f4{acc[i][c][4 * j], acc[i][c][4 * j + 1],
-                                                              acc[i][c][4 * j + 2], acc[i][c][4 * j + 3]};
-        return;
-    }
-    const uint32_t row0 = i0 + wi + (lane >> 5) * 4, col0 = c0 + wc + (lane & 31);
-    float cs[kTiles];
+                    out[((i * kTiles + c) * 4 + j) * 64] =
+                        f4{v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]};
+        } else if (direct) {
+            float* const o = p.dw + (i0 + wi + i * 32 + (lane >> 5) * 4) * p.dw_stride + col0;
 #pragma unroll
-    for (int c = 0; c < kTiles; ++c) cs[c] = column_scale<W>(p.col_scale, min(col0 + c * 32, p.cols - 1));
-    if (i0 + kTile <= p.n && c0 + kTile <= p.cols && !p.accumulate) {
-        float* const o = p.dw + row0 * p.dw_stride + col0;
+            for (int j = 0; j < 16; ++j)
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+                for (int c = 0; c < kTiles; ++c) o[((j >> 2) * 8 + (j & 3)) * p.dw_stride + c * 32] = v[c][j] * cs[c];
+        } else {
+            // An edge, or dw is added to: through LDS and a short loop.
+            // (Straight code for it is 20 KB that run once, and took 25 us to fetch.)
+            constexpr int kHere = kGroups == 1 ? 2 : 4;  // wavefronts in each array of stages
+            static_assert(sizeof(stages0) >= kHere * 32 * kWave * sizeof(float), "their rows fit");
+            const int w = group * 4 + wave;
+            float* const mine =
+                (w < kHere ? reinterpret_cast<float*>(stages0) : reinterpret_cast<float*>(stages1)) +
+                w % kHere * 32 * kWave;
+            __syncthreads();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
 #pragma unroll
                 for (int c = 0; c < kTiles; ++c)
-                    o[(i * 32 + (j >> 2) * 8 + (j & 3)) * p.dw_stride + c * 32] = acc[i][c][j] * cs[c];
-        return;
-    }
-    // An edge, or dw is added to: 32 rows at a time through LDS and a short
-    // loop.  (Straight code for it is 20 KB that run once, and took 25 us to
-    // fetch.)
-    float* const wave_out = reinterpret_cast<float*>(wave < 2 ? &stage0 : &stage1) + (wave & 1) * 32 * kWave;
-    static_assert(sizeof(Buffer) >= 2 * 32 * kWave * sizeof(float), "two wavefronts' rows fit a stage");
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-            for (int c = 0; c < kTiles; ++c)
-                wave_out[((lane >> 5) * 4 + (j >> 2) * 8 + (j & 3)) * kWave + (lane & 31) + c * 32] =
-                    acc[i][c][j] * cs[c];
-        __syncthreads();
+                    mine[((lane >> 5) * 4 + (j >> 2) * 8 + (j & 3)) * kWave + (lane & 31) + c * 32] = v[c][j] * cs[c];
+            __syncthreads();
 #pragma unroll 4
-        for (int e = lane; e < 32 * kWave; e += 64) {
-            const uint32_t r = i0 + wi + i * 32 + e / kWave, c = c0 + wc + e % kWave;
-            if (r < p.n && c < p.cols) {
-                float* const o = p.dw + r * p.dw_stride + c;
-                *o = p.accumulate ? *o + wave_out[e] : wave_out[e];
+            for (int e = lane; e < 32 * kWave; e += 64) {
+                const uint32_t r = i0 + wi + i * 32 + e / kWave, c = c0 + wc + e % kWave;
+                if (r < p.n && c < p.cols) {
+                    float* const o = p.dw + r * p.dw_stride + c;
+                    *o = p.accumulate ? *o + mine[e] : mine[e];
+                }
             }
         }
+    };
+    if constexpr (kGroups == 1) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) write(i, acc[i]);
+    } else {
+        // each group takes one row of parts: it gets the other group's sums of
+        // that row and gives its own of the other; the first group's come first
+        static_assert(kGroups == 2 && kTiles == 2, "a row of parts for each group");
+        static_assert(sizeof(stages0) >= kThreads * kGroups * sizeof(f16v), "one part's sums fit");
+        f4* const box = reinterpret_cast<f4*>(stages0);
+        f16v keep[kTiles];
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c) {
+            const f16v give = group ? acc[0][c] : acc[1][c];
+            keep[c] = group ? acc[1][c] : acc[0][c];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                box[(group * 4 + j) * kThreads + tid] =
+                    f4{give[4 * j], give[4 * j + 1], give[4 * j + 2], give[4 * j + 3]};
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f4 other = box[((group ^ 1) * 4 + j) * kThreads + tid];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) keep[c][4 * j + e] += other[e];
+            }
+        }
+        write(group, keep);
     }
 }
 
@@ -435,13 +470,12 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
 
 // The tile and into how many slices the rows are cut, by the least of an
 // estimate in microseconds.  Measured: 32 rows of a 256x256 tile take 0.8 us a
-// bfloat16 term of dy, one block a CU; of a 128x128 tile 0.43 us, or 0.7 us
-// with two blocks on a CU.  Slices fill the chip where the tiles do not (or
-// leave a last round mostly empty) and cost writing and reading their sums.
-// bf16, e4m3: 16384x4096x4096 takes 430 us in tiles of 256 and 580 in tiles of
-// 128, 4096x4096x1024 (64 tiles of 256 in 4 slices) 62 and 58, 2048x2048x2048
-// 47 and 31, 512x1024x4096 34 and 13; 8192x1024x1024 in tiles of 128 takes 94
-// in one slice and 36 in four.
+// bfloat16 term of dy, of a 128x128 tile 0.32 us, one block a CU.  Slices fill
+// the chip where the tiles do not (or leave a last round mostly empty) and cost
+// writing and reading their sums.  bf16, e4m3: 16384x4096x4096 takes 430 us in
+// tiles of 256 and 580 in tiles of 128, 4096x4096x1024 (64 tiles of 256 in 4
+// slices) 62 and 43, 2048x2048x2048 47 and 27, 512x1024x4096 34 and 13;
+// 8192x1024x1024 in tiles of 128 takes 94 in one slice and 32 in four.
 struct Shape {
     uint32_t tile, slices;
     uint64_t slice_rows, tiles_i, tiles_c;
@@ -454,9 +488,7 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms) {
         for (uint64_t k = 1; k <= 32 && (k == 1 || rows / k >= 128); ++k) {
             const uint64_t cut = ((rows + k - 1) / k + 63) / 64 * 64, slices = cut ? (rows + cut - 1) / cut : 0;
             const double blocks = (double)ti * (double)tc * (double)slices;
-            const double step = tile == 256 ? 0.8 * std::ceil(blocks / 256)
-                                            : blocks <= 256 ? 0.43 : 0.7 * std::ceil(blocks / 512);
-            double us = step * terms * (double)(cut / 32);
+            double us = (tile == 256 ? 0.8 : 0.32) * std::ceil(blocks / 256) * terms * (double)(cut / 32);
             if (slices > 1) us += 4.0 + (2.0 * slices + 1.0) * (double)n * (double)cols * 4.0 / 5.5e6;
             if (!best.tile || us < least) best = {tile, (uint32_t)slices, cut, ti, tc}, least = us;
         }
@@ -515,12 +547,13 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
                         using T = decltype(t);
                         using W = decltype(w);
                         constexpr int F = decltype(f)::value;
-                        // 64 rows a step are faster in the small tile of one term (59 us instead of 69
-                        // for 4096x4096x1024 int8), slower with more LDS in use (1142 -> 1525 us, fp16)
+                        // 64 rows a step are faster in the small tile of one term (59 us instead of 69 for
+                        // 4096x4096x1024 int8 in one group), slower with more LDS in use (1142 -> 1525, fp16
+                        // 16384x4096x4096)
                         if (s.tile == 256)
-                            k_weight_grad<T, W, F, 256, 32><<<grid, kThreads, 0, st>>>(p);
+                            k_weight_grad<T, W, F, 256, 32, 1><<<grid, kThreads, 0, st>>>(p);
                         else
-                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32><<<grid, kThreads, 0, st>>>(p);
+                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32, 2><<<grid, 2 * kThreads, 0, st>>>(p);
                     });
                 });
             });
