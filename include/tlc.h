@@ -436,7 +436,8 @@ int tlc_planes_scatter(const float* src, const uint64_t* src_off, float* dst, co
  * the largest code take it.  Every value a checkpoint stands for is 0 or a
  * normal, finite bfloat16 number.  A group of zeros has scale byte 0.  A group
  * with an infinity or a NaN has scale byte 255 and codes 0, and each of its
- * values decodes to NaN.
+ * values decodes to NaN.  Bytes that these calls do not write are not checked
+ * and stand for unspecified values.
  *
  * Matrices are row-major; consecutive columns are adjacent and rows lie a
  * stride (in elements, >= cols) apart, at any element: no alignment beyond the
@@ -524,8 +525,9 @@ int tlc_ckpt8_norm_grad(const void* dy, uint64_t dy_stride, const void* dsum, ui
  * rows dw_stride apart, for example a tensor's place in the flat buffer that
  * tlc_compress_group reads.  col_scale[cols], of dy's dtype or fp32, is
  * optional: the weight of the norm whose unweighted checkpoint x is.  Products are exact (dy
- * as one, two or three bfloat16 numbers for bf16, fp16, fp32), sums fp32 in a
- * fixed order.  rows == 0: dw becomes 0, or stays with accumulate.
+ * as one, two or three bfloat16 numbers for bf16, fp16, fp32; what of it lies
+ * below 2^-126 may count as 0), sums fp32 in a fixed order.  rows == 0: dw
+ * becomes 0, or stays with accumulate.
  * TLC_ERR_INVALID_ARG also for n and cols of more than 2^24 tiles of 128 x 128. */
 size_t tlc_ckpt8_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols);
 int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
