@@ -20,6 +20,7 @@ constexpr int kThreads = 256;  // of a group: four wavefronts, two by two
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
+typedef f4 f4_at4 __attribute__((aligned(4)));
 
 struct MatArgs {
     const void* dy;
@@ -117,6 +118,11 @@ __device__ __forceinline__ int swizzle(int t) { return (t & 3) << 2 | (t & 1); }
 
 __device__ __forceinline__ s4v read_tr(const uint16_t* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p);
+}
+// Orders a wavefront's own LDS accesses across its lanes.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 // Operand of a 32x32x16 product: `p` is the lane's place in rows k .. k+7 of
 // its half, with a read of rows +0..3 and one of rows +4..7.
@@ -371,37 +377,60 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
                 for (int j = 0; j < 4; ++j)
                     out[((i * kTiles + c) * 4 + j) * 64] =
                         f4{v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]};
-        } else if (direct) {
+            return;
+        }
+        if (direct) {
             float* const o = p.dw + (i0 + wi + i * 32 + (lane >> 5) * 4) * p.dw_stride + col0;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
 #pragma unroll
                 for (int c = 0; c < kTiles; ++c) o[((j >> 2) * 8 + (j & 3)) * p.dw_stride + c * 32] = v[c][j] * cs[c];
-        } else {
-            // An edge, or dw is added to: through LDS and a short loop.
-            // (Straight code for it is 20 KB that run once, and took 25 us to fetch.)
-            constexpr int kHere = kGroups == 1 ? 2 : 4;  // wavefronts in each array of stages
-            static_assert(sizeof(stages0) >= kHere * 32 * kWave * sizeof(float), "their rows fit");
-            const int w = group * 4 + wave;
-            float* const mine =
-                (w < kHere ? reinterpret_cast<float*>(stages0) : reinterpret_cast<float*>(stages1)) +
-                w % kHere * 32 * kWave;
-            __syncthreads();
+            return;
+        }
+        // An edge, or dw is added to: 32 rows through LDS, so that a lane has 16
+        // bytes of a row and eight reads of dw under way.  (8x8192x8192: 65 us
+        // directly and 77 so; added to, 422 by a loop of single values and 129
+        // so.)  Nothing reads the stages after the last meeting.
+        constexpr int kHere = kGroups == 1 ? 2 : 4;  // wavefronts in each array of stages
+        static_assert(sizeof(stages0) >= kHere * 32 * kWave * sizeof(float), "their rows fit");
+        const int w = group * 4 + wave;
+        float* const mine = (w < kHere ? reinterpret_cast<float*>(stages0) : reinterpret_cast<float*>(stages1)) +
+                            w % kHere * 32 * kWave;
+        if constexpr (kGroups == 2) __syncthreads();  // the sums' exchange is read
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 16; ++j)
 #pragma unroll
-                for (int c = 0; c < kTiles; ++c)
-                    mine[((lane >> 5) * 4 + (j >> 2) * 8 + (j & 3)) * kWave + (lane & 31) + c * 32] = v[c][j] * cs[c];
-            __syncthreads();
-#pragma unroll 4
-            for (int e = lane; e < 32 * kWave; e += 64) {
-                const uint32_t r = i0 + wi + i * 32 + e / kWave, c = c0 + wc + e % kWave;
-                if (r < p.n && c < p.cols) {
-                    float* const o = p.dw + r * p.dw_stride + c;
-                    *o = p.accumulate ? *o + mine[e] : mine[e];
-                }
+            for (int c = 0; c < kTiles; ++c)
+                mine[((lane >> 5) * 4 + (j >> 2) * 8 + (j & 3)) * kWave + (lane & 31) + c * 32] = v[c][j] * cs[c];
+        wave_sync();
+        const uint32_t r0 = i0 + wi + i * 32, w0 = c0 + wc;
+#pragma unroll 1
+        for (int q = 0; q < kWave / 8; q += 8) {
+            f4 old[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t e = ((q + u) * 64 + lane) * 4, r = r0 + e / kWave, c = w0 + e % kWave;
+                old[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+                if (p.accumulate && r < p.n && c + 4 <= p.cols)
+                    old[u] = *reinterpret_cast<const f4_at4*>(p.dw + r * p.dw_stride + c);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t e = ((q + u) * 64 + lane) * 4, r = r0 + e / kWave, c = w0 + e % kWave;
+                const f4 s = *reinterpret_cast<const f4*>(mine + e);
+                if (r < p.n && c + 4 <= p.cols)
+                    *reinterpret_cast<f4_at4*>(p.dw + r * p.dw_stride + c) = p.accumulate ? old[u] + s : s;
             }
         }
+        // the last one to three columns of the matrix, a row a lane
+        const uint32_t last = p.cols & ~3u;
+        if (lane < 32 && last >= w0 && last < w0 + kWave && r0 + lane < p.n)
+            for (uint32_t c = last; c < p.cols; ++c) {
+                float* const o = p.dw + (r0 + lane) * p.dw_stride + c;
+                const float s = mine[lane * kWave + c - w0];
+                *o = p.accumulate ? *o + s : s;
+            }
+        wave_sync();
     };
     if constexpr (kGroups == 1) {
 #pragma unroll
@@ -470,12 +499,13 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
 
 // The tile and into how many slices the rows are cut, by the least of an
 // estimate in microseconds.  Measured: 32 rows of a 256x256 tile take 0.8 us a
-// bfloat16 term of dy, of a 128x128 tile 0.32 us, one block a CU.  Slices fill
-// the chip where the tiles do not (or leave a last round mostly empty) and cost
-// writing and reading their sums.  bf16, e4m3: 16384x4096x4096 takes 430 us in
-// tiles of 256 and 580 in tiles of 128, 4096x4096x1024 (64 tiles of 256 in 4
-// slices) 62 and 43, 2048x2048x2048 47 and 27, 512x1024x4096 34 and 13;
-// 8192x1024x1024 in tiles of 128 takes 94 in one slice and 32 in four.
+// bfloat16 term of dy, of a 128x128 tile 0.32 us, one block a CU, and a tile's
+// beginning and end 14 and 5 us.  Slices fill the chip where the tiles do not
+// (or leave a last round mostly empty) and cost writing and reading their sums.
+// bf16, e4m3: 16384x4096x4096 takes 430 us in tiles of 256 and 580 in tiles of
+// 128, 4096x4096x1024 (64 tiles of 256 in 4 slices) 62 and 43, 2048x2048x2048
+// 47 and 27, 512x1024x4096 34 and 13; 8192x1024x1024 in tiles of 128 takes 94
+// in one slice and 32 in four.
 struct Shape {
     uint32_t tile, slices;
     uint64_t slice_rows, tiles_i, tiles_c;
@@ -485,15 +515,21 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms) {
     double least = 0.0;
     for (uint32_t tile = 128; tile <= 256; tile *= 2) {
         const uint64_t ti = (n + tile - 1) / tile, tc = (cols + tile - 1) / tile;
-        for (uint64_t k = 1; k <= 32 && (k == 1 || rows / k >= 128); ++k) {
+        for (uint64_t k : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (k > 1 && rows / k < 128) break;
             const uint64_t cut = ((rows + k - 1) / k + 63) / 64 * 64, slices = cut ? (rows + cut - 1) / cut : 0;
             const double blocks = (double)ti * (double)tc * (double)slices;
-            double us = (tile == 256 ? 0.8 : 0.32) * std::ceil(blocks / 256) * terms * (double)(cut / 32);
+            double us = std::ceil(blocks / 256) *
+                        (tile == 256 ? 14.0 + 0.8 * terms * (double)(cut / 32) : 5.0 + 0.32 * terms * (double)(cut / 32));
             if (slices > 1) us += 4.0 + (2.0 * slices + 1.0) * (double)n * (double)cols * 4.0 / 5.5e6;
             if (!best.tile || us < least) best = {tile, (uint32_t)slices, cut, ti, tc}, least = us;
         }
     }
     return best;
+}
+
+uint64_t workspace_of(const Shape& s) {
+    return s.slices > 1 ? s.slices * s.tiles_i * s.tiles_c * s.tile * s.tile * sizeof(float) : 256;
 }
 
 }  // namespace
@@ -502,12 +538,9 @@ extern "C" {
 
 size_t tlc_ckpt8_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols) {
     if (!valid_shape(rows, cols) || n < 1 || n > kMaxDim) return 0;
-    uint64_t bytes = 256;
-    for (int terms = 1; terms <= 3; ++terms) {  // of any dtype
-        const Shape s = shape_of(rows, n, cols, terms);
-        if (s.slices > 1)
-            bytes = std::max<uint64_t>(bytes, s.slices * s.tiles_i * s.tiles_c * s.tile * s.tile * sizeof(float));
-    }
+    uint64_t bytes = 0;
+    for (int terms = 1; terms <= 3; ++terms)  // of any dtype
+        bytes = std::max(bytes, workspace_of(shape_of(rows, n, cols, terms)));
     return bytes;
 }
 
@@ -523,9 +556,7 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
     if (!valid_weight(col_scale, col_scale_dtype, dtype)) return TLC_ERR_INVALID_ARG;
     if (((n + 127) / 128) * ((cols + 127) / 128) > (1u << 24)) return TLC_ERR_INVALID_ARG;
     const Shape s = shape_of(rows, n, cols, dtype == TLC_F32 ? 3 : dtype == TLC_F16 ? 2 : 1);
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < tlc_ckpt8_weight_grad_workspace_size(rows, n, cols))
-        return TLC_ERR_WORKSPACE;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_of(s)) return TLC_ERR_WORKSPACE;
     if (rows == 0 && accumulate) return TLC_OK;
     MatArgs p;
     p.dy = dy, p.dy_stride = dy_stride, p.codes = codes, p.scales = scales, p.rows = rows;

@@ -9,6 +9,7 @@ back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -1054,6 +1055,7 @@ def ckpt8_norm_grad(dy: torch.Tensor, saved, rstd: torch.Tensor, weight: torch.T
     return _on_stream(device, stream, body)
 
 
+@functools.lru_cache(maxsize=1024)
 def ckpt8_weight_grad_workspace_size(rows: int, n: int, cols: int) -> int:
     return int(lib().tlc_ckpt8_weight_grad_workspace_size(rows, n, cols))
 
