@@ -831,14 +831,15 @@ def _checkpoint(c: Checkpoint8, name: str, rows: int, cols: int, device):
     if c.cols != cols:
         raise ValueError(f"{name} must hold {cols} columns, got {c.cols}")
     groups = -(-cols // 32)
-    for t, what, width in ((c.codes, "codes", 32 * groups), (c.scales, "scales", -(-groups // 4) * 4)):
-        if not t.is_cuda or t.device != device:
-            raise ValueError(f"{name}.{what} must be on {device}, got {t.device}")
-        if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width \
-                or not t.is_contiguous():
-            raise ValueError(f"{name}.{what} must be contiguous uint8[{rows}, {width}], got "
-                             f"{tuple(t.shape)} of {t.dtype}")
-    return c.codes.data_ptr(), c.scales.data_ptr()
+    return (_bytes(c.codes, name, "codes", (rows, 32 * groups), device),
+            _bytes(c.scales, name, "scales", (rows, -(-groups // 4) * 4), device))
+
+
+def _bytes(t: torch.Tensor, name: str, what: str, shape: tuple, device) -> int:
+    if t.shape != shape or t.dtype != torch.uint8 or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}.{what} must be contiguous uint8{list(shape)} on a GPU, {device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 def _checkpoint_for(out: Checkpoint8 | None, name: str, rows: int, cols: int, fmt: int, device):
@@ -857,7 +858,7 @@ def _matrix_for(out: torch.Tensor | None, name: str, like: torch.Tensor):
     """(matrix, pointer, row stride): `out`, checked, or a new one of like's shape and dtype."""
     if out is not None:
         return (out, *_matrix(out, name, like))
-    out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    out = torch.empty_like(like, memory_format=torch.contiguous_format)
     return out, out.data_ptr(), like.shape[1]
 
 
@@ -1010,6 +1011,7 @@ def ckpt8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, fmt: in
     return _on_stream(device, stream, body)
 
 
+@functools.lru_cache(maxsize=1024)
 def ckpt8_norm_grad_workspace_size(rows: int, cols: int) -> int:
     return int(lib().tlc_ckpt8_norm_grad_workspace_size(rows, cols))
 
