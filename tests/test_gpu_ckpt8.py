@@ -486,7 +486,9 @@ def test_weight_gradient(tlc, fmt, dtype):
 def test_weight_gradient_of_many_tiles_is_exact(tlc, fmt, dtype):
     """Sizes that take the larger tile, alone and in slices, with and without ragged edges; whole numbers, so that
     every sum has one right value (below 2^24)."""
-    for k, (rows, n, cols) in enumerate([(300, 4000, 4100), (2000, 2100, 2000), (330, 4096, 4096), (700, 2048, 2048)]):
+    sizes = [(300, 4000, 4100), (2000, 2100, 2000), (330, 4096, 4096), (700, 2048, 2048), (4096, 2100, 2050),
+             (2100, 4000, 4000)]
+    for k, (rows, n, cols) in enumerate(sizes):
         say(f"case weight_grad many tiles {rows}x{n}x{cols} {dtype} format {fmt}")
         g = torch.Generator(device="cuda").manual_seed(k)
         dy = torch.randint(-9, 10, (rows, n + 5), generator=g, device="cuda").to(dtype)[:, 3:n + 3]
