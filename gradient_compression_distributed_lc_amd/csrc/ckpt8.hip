@@ -16,6 +16,7 @@ namespace {
 
 using namespace tlc_ckpt8;
 using tlc_internal::launch;
+using tlc_internal::launch_blocks;
 
 constexpr int kThreads = 256;
 
@@ -82,6 +83,7 @@ __device__ __forceinline__ float act_p(float x, float* slope) {
 
 struct Walk {
     uint64_t units;       // rows * per_row
+    uint64_t first;       // block of the whole that the launch begins with
     uint64_t magic;       // ceil(2^64 / per_row): row of a unit below 2^32
     uint32_t per_row;     // 4 * ceil(cols / 32)
     uint32_t magic32;     // ceil(2^32 / per_row): rows inside a block
@@ -93,6 +95,7 @@ inline Walk walk_of(uint64_t rows, uint64_t cols) {
     Walk w;
     w.per_row = (uint32_t)(4 * groups_of(cols));
     w.units = rows * w.per_row;
+    w.first = 0;
     w.magic = ~0ull / w.per_row + 1;
     w.magic32 = 0xFFFFFFFFu / w.per_row + 1;
     w.cols = (uint32_t)cols;
@@ -108,7 +111,7 @@ struct Place {
 
 template <int U>
 __device__ __forceinline__ void places(const Walk& w, Place* at) {
-    const uint64_t first = (uint64_t)blockIdx.x * (kThreads * U);
+    const uint64_t first = (w.first + blockIdx.x) * (kThreads * U);
     const uint64_t row0 = first >> 32 ? first / w.per_row : __umul64hi(first, w.magic);
     const uint32_t unit0 = (uint32_t)(first - row0 * w.per_row);
 #pragma unroll
@@ -635,10 +638,15 @@ int with_saved(int format, Fn&& fn) {
     return format ? with_format(format, fn) : fn(Int<0>{});
 }
 
-// Blocks of a walk with U units a lane; 0: too many for one launch.
-uint32_t walk_blocks(const Walk& w, uint64_t per_block) {
-    const uint64_t b = (w.units + per_block - 1) / per_block;
-    return b > 0x7FFFFFFFull ? 0 : (uint32_t)b;
+// Launches a kernel over a walk with `per_lane` units a lane: fn(walk, blocks).
+template <typename Fn>
+int launch_walk(const char* name, hipStream_t st, Walk w, uint64_t per_lane, Fn&& fn) {
+    const uint64_t per_block = kThreads * per_lane;
+    return launch_blocks(name, st, (w.units + per_block - 1) / per_block, kThreads,
+                         [&](uint64_t first, uint32_t blocks) {
+                             w.first = first;
+                             fn(w, blocks);
+                         });
 }
 
 template <typename Fn>
@@ -659,9 +667,7 @@ int run_act(int inputs, int act, const void* a, uint64_t a_stride, const void* b
     if (inputs >= 1 && !valid_matrix(y, dtype, cols, y_stride)) return TLC_ERR_INVALID_ARG;
     if (inputs == 2 && (!valid_matrix(b, dtype, cols, b_stride) || !valid_checkpoint(b_codes, b_scales)))
         return TLC_ERR_INVALID_ARG;
-    const Walk w = walk_of(rows, cols);
-    const uint32_t blocks = walk_blocks(w, kThreads * 2);
-    if (!blocks) return TLC_ERR_INVALID_ARG;
+    const Walk walk = walk_of(rows, cols);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         using E = typename T::Elem;
@@ -671,13 +677,13 @@ int run_act(int inputs, int act, const void* a, uint64_t a_stride, const void* b
             const E* const pb = static_cast<const E*>(b);
             E* const py = static_cast<E*>(y);
             if (inputs == 0)
-                return launch("tlc_ckpt8_pack", st, [&] {
+                return launch_walk("tlc_ckpt8_pack", st, walk, 2, [&](const Walk& w, uint32_t blocks) {
                     k_act<T, F, TLC_ACT_SILU, 0><<<blocks, kThreads, 0, st>>>(w, pa, a_stride, nullptr, 0, nullptr, 0,
                                                                              a_codes, a_scales, nullptr, nullptr);
                 });
             return with_act(act, [&](auto k) {
                 constexpr int A = decltype(k)::value;
-                return launch("tlc_ckpt8_act", st, [&] {
+                return launch_walk("tlc_ckpt8_act", st, walk, 2, [&](const Walk& w, uint32_t blocks) {
                     if (inputs == 1)
                         k_act<T, F, A, 1><<<blocks, kThreads, 0, st>>>(w, pa, a_stride, nullptr, 0, py, y_stride,
                                                                        a_codes, a_scales, nullptr, nullptr);
@@ -708,14 +714,12 @@ int tlc_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int format, ui
     if (!valid_dtype(dtype) || !valid_format(format) || !valid_shape(rows, cols)) return TLC_ERR_INVALID_ARG;
     if (rows == 0) return TLC_OK;
     if (!valid_matrix(y, dtype, cols, y_stride) || !valid_checkpoint(codes, scales)) return TLC_ERR_INVALID_ARG;
-    const Walk w = walk_of(rows, cols);
-    const uint32_t blocks = walk_blocks(w, kThreads * 2);
-    if (!blocks) return TLC_ERR_INVALID_ARG;
+    const Walk walk = walk_of(rows, cols);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         return with_format(format, [&](auto f) {
-            return launch("tlc_ckpt8_unpack", st, [&] {
+            return launch_walk("tlc_ckpt8_unpack", st, walk, 2, [&](const Walk& w, uint32_t blocks) {
                 k_unpack<T, decltype(f)::value>
                     <<<blocks, kThreads, 0, st>>>(w, codes, scales, static_cast<typename T::Elem*>(y), y_stride);
             });
@@ -745,9 +749,7 @@ int tlc_ckpt8_act_grad(int act, const uint8_t* a_codes, const uint8_t* a_scales,
     if (gated && (!valid_matrix(db, dtype, cols, db_stride) || !valid_checkpoint(b_codes, b_scales)))
         return TLC_ERR_INVALID_ARG;
     if ((y_codes || y_scales) && !valid_checkpoint(y_codes, y_scales)) return TLC_ERR_INVALID_ARG;
-    const Walk w = walk_of(rows, cols);
-    const uint32_t blocks = walk_blocks(w, kThreads * (gated ? 1 : 2));
-    if (!blocks) return TLC_ERR_INVALID_ARG;
+    const Walk walk = walk_of(rows, cols);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
@@ -756,7 +758,7 @@ int tlc_ckpt8_act_grad(int act, const uint8_t* a_codes, const uint8_t* a_scales,
             constexpr int F = decltype(f)::value;
             return with_act(act, [&](auto k) {
                 constexpr int A = decltype(k)::value;
-                return launch("tlc_ckpt8_act_grad", st, [&] {
+                return launch_walk("tlc_ckpt8_act_grad", st, walk, gated ? 1 : 2, [&](const Walk& w, uint32_t blocks) {
                     if (gated)
                         k_act_grad<T, F, A, true><<<blocks, kThreads, 0, st>>>(
                             w, a_codes, a_scales, b_codes, b_scales, static_cast<const E*>(dy), dy_stride,

@@ -5,8 +5,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <vector>
 
@@ -41,6 +43,20 @@ int launch(const char* name, hipStream_t st, Launch&& fn) {
         if (hipEventRecord(b, st) != hipSuccess) return TLC_ERR_HIP;
         std::lock_guard<std::mutex> lk(g_prof_mu);
         g_prof.push_back({name, a, b});
+    }
+    return TLC_OK;
+}
+
+// The same for `blocks` blocks of `threads` threads that may be too many for
+// one launch: HIP refuses 2^32 threads, and past them runs what is left modulo
+// 2^32 without an error.  Calls fn(first block, blocks of this launch).
+template <typename Launch>
+int launch_blocks(const char* name, hipStream_t st, uint64_t blocks, uint32_t threads, Launch&& fn) {
+    const uint64_t most = 0xFFFFFFFFull / threads;
+    for (uint64_t first = 0; first < blocks; first += most) {
+        const uint32_t here = (uint32_t)std::min(most, blocks - first);
+        const int rc = launch(name, st, [&] { fn(first, here); });
+        if (rc) return rc;
     }
     return TLC_OK;
 }

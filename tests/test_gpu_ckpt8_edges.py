@@ -1,0 +1,77 @@
+"""Edges of the 8-bit checkpoint operators: the tails of the activation
+functions, roundings counted one by one, every code in the weight gradient,
+and sizes of more than one launch.
+
+u(dtype) is half a step of a type relative to the value, as in
+test_gpu_ckpt8.py, whose definitions in 64 bits are used here too."""
+import math
+
+import pytest
+import torch
+
+import ckpt8_ref as ref
+from gpu_util import say
+from test_gpu_ckpt8 import LEAST, U, assert_close, gen, randn, to_ck
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [ref.INT8, ref.E4M3]
+
+
+@pytest.fixture(scope="module")
+def tlc():
+    from gradient_compression_distributed_lc_amd import tlc
+    return tlc
+
+
+# ---- more than one launch ---------------------------------------------------
+#
+# HIP refuses a launch of 2^32 threads; the elementwise calls give a thread two
+# units of eight columns (one in the gated gradient), the norm a row of up to
+# 512 columns to a wavefront, the weight gradient a tile to 512 threads.
+
+
+def ends(n, k=1000):
+    """The first and last k rows, and k around the middle."""
+    return [slice(0, k), slice(n // 2 - k, n // 2), slice(n - k, n)]
+
+
+def rows_of(c, at):
+    return type(c)(c.codes[at], c.scales[at], c.cols, c.format)
+
+
+def test_elementwise_calls_of_more_than_one_launch(tlc):
+    rows = 2 ** 31 - 1  # four units a row
+    say(f"case elementwise {rows}x1")
+    x = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    for at in ends(rows):
+        x[at] = torch.linspace(-3, 3, 1000, device="cuda").to(torch.bfloat16).unsqueeze(1)
+    c = tlc.ckpt8_pack(x, ref.INT8)
+    for at in ends(rows):
+        alone = tlc.ckpt8_pack(x[at], ref.INT8)
+        assert torch.equal(c.codes[at], alone.codes) and torch.equal(c.scales[at], alone.scales)
+    y = tlc.ckpt8_unpack(c)
+    for at in ends(rows):
+        assert torch.equal(y[at], tlc.ckpt8_unpack(rows_of(c, at)))
+    tlc.ckpt8_act_grad(x, ref.SILU, c, da=y)
+    for at in ends(rows):
+        assert torch.equal(y[at], tlc.ckpt8_act_grad(x[at], ref.SILU, rows_of(c, at))[0])
+    c.codes.zero_()
+    tlc.ckpt8_act(x, ref.SILU, ref.INT8, y=y, a_out=c)
+    for at in ends(rows):
+        want, alone, _ = tlc.ckpt8_act(x[at], ref.SILU, ref.INT8)
+        assert torch.equal(y[at], want) and torch.equal(c.codes[at], alone.codes)
+
+
+def test_gated_gradient_of_more_than_one_launch(tlc):
+    rows = 2 ** 30 + 5
+    say(f"case gated gradient {rows}x1")
+    a = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda").fill_(1.0)
+    for at in ends(rows):
+        a[at] = torch.linspace(-3, 3, 1000, device="cuda").to(torch.bfloat16).unsqueeze(1)
+    c = tlc.ckpt8_pack(a, ref.E4M3)
+    da, db, cy = tlc.ckpt8_act_grad(a, ref.GELU, c, c, want_y=True)
+    for at in ends(rows):
+        want = tlc.ckpt8_act_grad(a[at], ref.GELU, rows_of(c, at), rows_of(c, at), want_y=True)
+        assert torch.equal(da[at], want[0]) and torch.equal(db[at], want[1])
+        assert torch.equal(cy.codes[at], want[2].codes) and torch.equal(cy.scales[at], want[2].scales)
