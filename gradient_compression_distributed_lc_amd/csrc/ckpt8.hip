@@ -340,6 +340,7 @@ struct NormArgs {
     uint8_t *codes, *scales;
     float* rstd;
     uint64_t rows;
+    uint64_t first;                   // block of the whole that the launch begins with
     uint32_t cols, units, scale_row;  // units of a row, pads among them
     int waves;
 };
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
     using Elem = typename T::Elem;
     __shared__ double sm[16];
     const int wave = threadIdx.x >> 6, rows_here = max(1, (int)(blockDim.x >> 6) / p.waves);
-    const uint64_t row = (uint64_t)blockIdx.x * rows_here + wave / p.waves;
+    const uint64_t row = (p.first + blockIdx.x) * rows_here + wave / p.waves;
     const bool live = row < p.rows;
     const uint32_t lane = (wave % p.waves) * 64 + (threadIdx.x & 63), lanes = p.waves * 64;
     float v[kVec][8];
@@ -796,13 +797,14 @@ int tlc_ckpt8_norm(const void* x, uint64_t x_stride, const void* residual, uint6
     p.codes = codes, p.scales = scales, p.rstd = rstd, p.rows = rows;
     p.cols = (uint32_t)cols, p.units = (uint32_t)(4 * groups_of(cols)), p.scale_row = (uint32_t)scale_stride(cols);
     p.waves = s.waves;
-    const uint32_t blocks = (uint32_t)((rows + s.rows_here - 1) / s.rows_here);
+    const uint64_t all = (rows + s.rows_here - 1) / s.rows_here;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
         return with_weight(t, weight, weight_dtype, [&](auto w) {
             return with_format(format, [&](auto f) {
                 return with_vec(s.vec, [&](auto v) {
-                    return launch("tlc_ckpt8_norm", st, [&] {
+                    return launch_blocks("tlc_ckpt8_norm", st, all, s.threads, [&](uint64_t first, uint32_t blocks) {
+                        p.first = first;
                         k_norm<decltype(t), decltype(w), decltype(f)::value, decltype(v)::value>
                             <<<blocks, s.threads, 0, st>>>(p);
                     });

@@ -75,3 +75,22 @@ def test_gated_gradient_of_more_than_one_launch(tlc):
         want = tlc.ckpt8_act_grad(a[at], ref.GELU, rows_of(c, at), rows_of(c, at), want_y=True)
         assert torch.equal(da[at], want[0]) and torch.equal(db[at], want[1])
         assert torch.equal(cy.codes[at], want[2].codes) and torch.equal(cy.scales[at], want[2].scales)
+
+
+def test_norm_of_more_than_one_launch(tlc):
+    rows, cols = 2 ** 26 + 5, 2
+    say(f"case norm {rows}x{cols}")
+    x = torch.ones(rows, cols, device="cuda")
+    r = torch.ones(rows, cols, device="cuda")
+    for at in ends(rows):
+        r[at] = randn(gen(at.stop % 7), 1000, cols).cuda()
+    w = torch.tensor([0.5, 3.0], device="cuda")
+    total, y, c, rstd = tlc.ckpt8_norm(x, w, 1e-5, ref.INT8, residual=r)
+    for at in ends(rows):
+        t1, y1, c1, r1 = tlc.ckpt8_norm(x[at], w, 1e-5, ref.INT8, residual=r[at])
+        assert torch.equal(total[at], t1) and torch.equal(y[at], y1) and torch.equal(rstd[at], r1)
+        assert torch.equal(c.codes[at], c1.codes) and torch.equal(c.scales[at], c1.scales)
+    # its gradient walks over the rows with a bounded number of blocks
+    dx, _ = tlc.ckpt8_norm_grad(r, c, rstd, w)
+    for at in ends(rows):
+        assert torch.equal(dx[at], tlc.ckpt8_norm_grad(r[at], rows_of(c, at), rstd[at], w)[0])
