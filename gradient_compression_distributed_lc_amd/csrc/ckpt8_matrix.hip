@@ -13,7 +13,7 @@
 namespace {
 
 using namespace tlc_ckpt8;
-using tlc_internal::launch;
+using tlc_internal::launch_blocks;
 
 constexpr int kThreads = 256;  // of a group: four wavefronts, two by two
 
@@ -36,6 +36,7 @@ struct MatArgs {
     f4* partial;         // with several: [slices][tiles], each tile as its lanes hold it; else nullptr
     uint64_t slice_rows; // rows of one slice, a multiple of 64
     uint32_t tiles, tiles_i, tiles_c;  // tiles of dw, its rows of them, and those of one row
+    uint32_t first;      // block of the whole that the launch begins with
 };
 
 // Place in the matrix of tile number `tile`: neighbours in bands of 4 rows of tiles.
@@ -166,6 +167,7 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
     uint32_t b = blockIdx.x;
     const uint32_t total = gridDim.x, per = total / 8;
     if (b < per * 8) b = b % 8 * per + b / 8;
+    b += p.first;
     const uint32_t slice = b / p.tiles, tile = b % p.tiles;
     uint32_t tile_i, tile_c;
     tile_place(p, tile, &tile_i, &tile_c);
@@ -467,7 +469,8 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
 template <typename W>
 __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t slices, uint32_t tile_size) {
     const uint32_t per = tile_size * tile_size / 4;  // f4 of a tile
-    const uint32_t tile = blockIdx.x / (per / kThreads), v = blockIdx.x % (per / kThreads) * kThreads + threadIdx.x;
+    const uint32_t b = p.first + blockIdx.x;
+    const uint32_t tile = b / (per / kThreads), v = b % (per / kThreads) * kThreads + threadIdx.x;
     const f4* const in = p.partial + (uint64_t)tile * per + v;
     const uint64_t next = (uint64_t)p.tiles * per;
     f4 s = {};
@@ -570,31 +573,35 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
     p.tiles_i = (uint32_t)s.tiles_i, p.tiles_c = (uint32_t)s.tiles_c;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (s.slices) {
-        const uint32_t grid = p.tiles * s.slices;
+        const uint64_t all = (uint64_t)p.tiles * s.slices;
+        const uint32_t threads = s.tile == 256 ? kThreads : 2 * kThreads;
         const int rc = with_dtype(dtype, [&](auto t) {
             return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
                 return with_format(format, [&](auto f) {
-                    return launch("tlc_ckpt8_weight_grad", st, [&] {
+                    return launch_blocks("tlc_ckpt8_weight_grad", st, all, threads, [&](uint64_t first,
+                                                                                         uint32_t blocks) {
                         using T = decltype(t);
                         using W = decltype(w);
                         constexpr int F = decltype(f)::value;
+                        p.first = (uint32_t)first;
                         // 64 rows a step are faster in the small tile of one term (59 us instead of 69 for
                         // 4096x4096x1024 int8 in one group), slower with more LDS in use (1142 -> 1525, fp16
                         // 16384x4096x4096)
                         if (s.tile == 256)
-                            k_weight_grad<T, W, F, 256, 32, 1><<<grid, kThreads, 0, st>>>(p);
+                            k_weight_grad<T, W, F, 256, 32, 1><<<blocks, threads, 0, st>>>(p);
                         else
-                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32, 2><<<grid, 2 * kThreads, 0, st>>>(p);
+                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32, 2><<<blocks, threads, 0, st>>>(p);
                     });
                 });
             });
         });
         if (rc || s.slices == 1) return rc;
     }
-    const uint32_t blocks = p.tiles * (s.tile * s.tile / 4 / kThreads);
+    const uint64_t all = (uint64_t)p.tiles * (s.tile * s.tile / 4 / kThreads);
     return with_dtype(dtype, [&](auto t) {
         return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
-            return launch("tlc_ckpt8_weight_sum", st, [&] {
+            return launch_blocks("tlc_ckpt8_weight_sum", st, all, kThreads, [&](uint64_t first, uint32_t blocks) {
+                p.first = (uint32_t)first;
                 k_weight_sum<decltype(w)><<<blocks, kThreads, 0, st>>>(p, s.slices, s.tile);
             });
         });

@@ -94,3 +94,21 @@ def test_norm_of_more_than_one_launch(tlc):
     dx, _ = tlc.ckpt8_norm_grad(r, c, rstd, w)
     for at in ends(rows):
         assert torch.equal(dx[at], tlc.ckpt8_norm_grad(r[at], rows_of(c, at), rstd[at], w)[0])
+
+
+def test_weight_gradient_of_more_than_one_launch(tlc):
+    cols = 2 ** 30 + 300  # 2^23 + 3 tiles of 128
+    say(f"case weight_grad 1x1x{cols}")
+    x = torch.ones(1, cols, dtype=torch.bfloat16, device="cuda")
+    for at in ends(cols):
+        x[0, at] = torch.randint(-7, 8, (1000,), generator=gen(at.stop % 7)).cuda().to(torch.bfloat16)
+    c = tlc.ckpt8_pack(x, ref.INT8)
+    dy = torch.full((1, 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    dw = tlc.ckpt8_weight_grad(dy, c)
+    for at in ends(cols):
+        assert torch.equal(dw[0, at], 3 * x[0, at].float())
+    assert float(dw.min()) == -21.0 and float(dw.max()) == 21.0
+    # no rows: the same matrix is set to 0
+    none = tlc.Checkpoint8(c.codes[:0], c.scales[:0], cols, ref.INT8)
+    tlc.ckpt8_weight_grad(dy[:0], none, dw=dw)
+    assert not dw.any()
