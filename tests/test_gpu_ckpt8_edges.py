@@ -24,6 +24,46 @@ def tlc():
     return tlc
 
 
+# In 16 bits x*x is exact (at most 22 bits), so P(x) = exp(-x^2/2) * h(|x|) is
+# off by the exponent's two roundings (constant and product: x^2/2 * 1.5 *
+# 2^-24), and by less than 12 * 2^-24 for the hardware's exp2 and reciprocal,
+# the fit (1.4 * 2^-24) and the polynomial's roundings.
+def tail_bound(x64):
+    return (0.75 * x64 * x64 + 12) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_gelu_in_the_negative_tail_is_right_relative_to_its_value(tlc, dtype):
+    """Every value of the type between -13 and -3: f and f' fall to 1e-37 there, and each keeps the type's precision."""
+    x = torch.arange(-13.0, -3.0, 2.0 ** -9).to(dtype).unique()
+    x = torch.nn.functional.pad(x, (0, -x.numel() % 32), value=-3.0).view(-1, 32)  # sorted: a group is a short range
+    rows, cols = x.shape
+    for fmt in FORMATS:
+        say(f"case gelu tail {rows}x{cols} {dtype} format {fmt}")
+        b = torch.full_like(x, 2.0)
+        y, ca, cb = tlc.ckpt8_act(x.cuda(), ref.GELU, fmt, b=b.cuda())
+        want = ref.act(ref.GELU, x.double())[0] * 2
+        assert_close(y, want, (U[dtype] * 1.01 + tail_bound(x.double())) * want.abs() + LEAST[dtype], "y")
+        # the gradients and y in 8 bits, at the checkpoint's values
+        dy = torch.ones(rows, cols, dtype=torch.float32, device="cuda").to(dtype)
+        da, db, cy = tlc.ckpt8_act_grad(dy, ref.GELU, ca, cb, want_y=True)
+        a = ref.decode(*ref.encode(x.double(), fmt), fmt, cols)
+        f, slope = ref.act(ref.GELU, a)
+        assert_close(db, f, (U[dtype] * 1.01 + tail_bound(a)) * f.abs() + LEAST[dtype], "db")
+        # f' = P + x*phi: |x*phi| is above nine times P, so what either is off by counts 10/8 of the sum at most
+        want = 2 * slope
+        assert_close(da, want, (U[dtype] * 1.01 + 1.25 * (tail_bound(a) + 4 * 2.0 ** -24)) * want.abs() + LEAST[dtype],
+                     "da")
+        y64 = 2 * f
+        codes, scales = ref.encode(y64, fmt)
+        got_scales = cy.scales.cpu()
+        assert torch.equal(got_scales, scales)
+        s = torch.exp2(scales[:, :1].double() - 127)
+        half = s / 2 if fmt == ref.INT8 else torch.maximum(y64.abs() * 2.0 ** -4, s * 2.0 ** -10)
+        got = ref.decode(cy.codes.cpu(), got_scales, fmt, cols)
+        assert ((got - y64).abs() <= half * 1.0001 + tail_bound(a) * y64.abs()).all(), "y in 8 bits"
+
+
 # ---- more than one launch ---------------------------------------------------
 #
 # HIP refuses a launch of 2^32 threads; the elementwise calls give a thread two
