@@ -40,10 +40,29 @@ __device__ __forceinline__ float fast_logistic(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
 
+// The logistic function of u, and with kBoth that of -u in *rest: of
+// 1/(1 + e^-|u|) and e^-|u|/(1 + e^-|u|) neither cancels, where 1 - p would be
+// off by 2^-25 however small it is (times x*u' in the slope of gelu_tanh,
+// hundreds of roundings of it in fp32).  16-bit tensors take 1 - p: 2^-24 of
+// x*u', which is below 40 where 1 - p is not 0 yet, is a hundredth of their
+// rounding.
+template <bool kPrecise, bool kBoth>
+__device__ __forceinline__ float logistic(float u, float* rest) {
+    if constexpr (!kPrecise) {
+        const float p = fast_logistic(u);
+        if constexpr (kBoth) *rest = 1.0f - p;
+        return p;
+    } else {
+        const float e = expf(-fabsf(u)), high = 1.0f / (1.0f + e), low = e * high;
+        if constexpr (kBoth) *rest = u < 0.0f ? high : low;
+        return u < 0.0f ? low : high;
+    }
+}
+
 // P(x), and with kSlope also f'(x).
 template <int A, bool kPrecise, bool kSlope>
 __device__ __forceinline__ float act_p(float x, float* slope) {
-    float p;
+    float p, q;  // q: the logistic function of the negative argument
     if constexpr (A == TLC_ACT_GELU) {
         float g;  // exp(-x^2/2)
         if constexpr (kPrecise) {
@@ -67,14 +86,14 @@ __device__ __forceinline__ float act_p(float x, float* slope) {
         // past 30 the logistic function is 0 or 1, and the cube would overflow later
         const float c = x != x ? x : fminf(fmaxf(x, -30.0f), 30.0f), cc = c * c;
         const float u = 2.0f * kTanhScale * c * fmaf(0.044715f, cc, 1.0f);
-        p = kPrecise ? 1.0f / (1.0f + expf(-u)) : fast_logistic(u);
+        p = logistic<kPrecise, kSlope>(u, &q);
         if constexpr (kSlope) {
             const float du = 2.0f * kTanhScale * fmaf(0.134145f, cc, 1.0f);
-            *slope = fmaf(c * p * (1.0f - p), du, p);
+            *slope = fmaf(c * p * q, du, p);
         }
     } else {
-        p = kPrecise ? 1.0f / (1.0f + expf(-x)) : fast_logistic(x);
-        if constexpr (kSlope) *slope = fmaf(x * p, 1.0f - p, p);
+        p = logistic<kPrecise, kSlope>(x, &q);
+        if constexpr (kSlope) *slope = fmaf(x * p, q, p);
     }
     return p;
 }

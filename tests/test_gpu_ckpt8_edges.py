@@ -64,6 +64,25 @@ def test_gelu_in_the_negative_tail_is_right_relative_to_its_value(tlc, dtype):
         assert ((got - y64).abs() <= half * 1.0001 + tail_bound(a) * y64.abs()).all(), "y in 8 bits"
 
 
+def test_gelu_tanh_gradient_in_fp32_counts_roundings(tlc):
+    """f' = p + x*u'*p*q with p and q the logistic function of u and -u, both without a cancellation: u (below 4
+    roundings) moves p by p*q*|u| of them and p*q by as much of itself, and the products round a few times more.
+    1 - p taken from p rounded to 24 bits would be off by x*u'*2^-25, hundreds of roundings of the result."""
+    x = torch.cat([torch.linspace(-9, 9, 2048), torch.linspace(-40, 40, 2048)]).view(-1, 32)
+    k, e = math.sqrt(2 / math.pi), 2.0 ** -24
+    for fmt in FORMATS:
+        say(f"case gelu_tanh gradient {tuple(x.shape)} format {fmt}")
+        c = tlc.ckpt8_pack(x.cuda(), fmt)
+        a = ref.decode(*ref.encode(x.double(), fmt), fmt, 32)
+        da, _, _ = tlc.ckpt8_act_grad(torch.ones_like(x).cuda(), ref.GELU_TANH, c)
+        u = 2 * k * (a + 0.044715 * a ** 3)
+        p, q = torch.sigmoid(u), torch.sigmoid(-u)
+        part = a * 2 * k * (1 + 3 * 0.044715 * a * a) * p * q
+        want = p + part
+        bound = e * (want.abs() + p * (4 + 4 * u.abs() * q) + part.abs() * (12 + 8 * u.abs())) + 2.0 ** -126
+        assert_close(da, want, bound, "da")
+
+
 # ---- more than one launch ---------------------------------------------------
 #
 # HIP refuses a launch of 2^32 threads; the elementwise calls give a thread two
