@@ -447,8 +447,13 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs p) {
             float o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j] = v[i][j] * rstd32;
-                if (p.weight) o[j] *= w[j];
+                if constexpr (T::kTerms == 3) {  // one rounding
+                    const double n = (double)v[i][j] * rstd;
+                    o[j] = (float)(p.weight ? n * (double)w[j] : n);
+                } else {  // 3 * 2^-24 beside the type's own rounding (16384x4096 bf16 100 us, 105 in 64 bits)
+                    o[j] = v[i][j] * rstd32;
+                    if (p.weight) o[j] *= w[j];
+                }
             }
             store8<T>(static_cast<Elem*>(p.y) + row * p.y_stride + unit * 8ull, n, pack8<T>(o));
         }

@@ -83,6 +83,22 @@ def test_gelu_tanh_gradient_in_fp32_counts_roundings(tlc):
         assert_close(da, want, bound, "da")
 
 
+def test_norm_output_in_fp32_is_rounded_once(tlc):
+    """y = sum*rstd*weight from 64 bits: off by half a step, with a weight and without."""
+    for k, (rows, cols) in enumerate([(1, 1), (7, 33), (64, 515), (9, 4096), (5, 9000)]):
+        say(f"case norm fp32 {rows}x{cols}")
+        g = gen(500 + k)
+        x, r, w = randn(g, rows, cols), randn(g, rows, cols, scale=3.0), 1 + randn(g, cols, scale=0.3)
+        total = x + r
+        _, n = ref.norm(total.double(), float(torch.tensor(1e-5)))
+        for fmt in (None, *FORMATS):
+            for weight in (w, None):
+                _, y, _, _ = tlc.ckpt8_norm(x.cuda(), None if weight is None else weight.cuda(), 1e-5, fmt,
+                                            residual=r.cuda())
+                want = n if weight is None else n * weight.double()
+                assert_close(y, want, want.abs() * 2.0 ** -24 * 1.0001 + LEAST[torch.float32], "y")
+
+
 # ---- more than one launch ---------------------------------------------------
 #
 # HIP refuses a launch of 2^32 threads; the elementwise calls give a thread two
