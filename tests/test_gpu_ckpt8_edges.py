@@ -99,6 +99,57 @@ def test_norm_output_in_fp32_is_rounded_once(tlc):
                 assert_close(y, want, want.abs() * 2.0 ** -24 * 1.0001 + LEAST[torch.float32], "y")
 
 
+# ---- every code in the weight gradient ----------------------------------------
+
+
+def one_hot(rows, n, dtype):
+    dy = torch.zeros(rows, n, dtype=dtype)
+    dy[torch.arange(rows), torch.arange(rows) % n] = 1.0
+    return dy
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_weight_gradient_reads_every_code_at_every_scale(tlc, fmt, dtype):
+    """dy of one 1 a row: dw is the checkpoint's values themselves, from every code at the least, the largest and all
+    scales between, in the small tile and in the large one."""
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes = codes[(codes & 127) != 127] if fmt == ref.E4M3 else codes[codes != 128]
+    codes = torch.nn.functional.pad(codes, (0, 256 - codes.numel())).view(1, 256)
+    lo, hi = ref.LOW[fmt] + 127, ref.HIGH[fmt] + 127
+    scales = torch.arange(lo, hi + 1, dtype=torch.uint8)
+    rows = scales.numel()
+    for n, wide in ((rows, 1), (4096, 16)):
+        say(f"case weight_grad codes {rows}x{n}x{256 * wide} {dtype} format {fmt}")
+        all_codes, all_scales = codes.repeat(rows, wide), scales.view(-1, 1).repeat(1, 8 * wide)
+        want = ref.decode(all_codes, all_scales, fmt, 256 * wide)
+        got = tlc.ckpt8_weight_grad(one_hot(rows, n, dtype).cuda(), to_ck(tlc, all_codes, all_scales, 256 * wide, fmt))
+        assert torch.equal(got[:rows].cpu().double(), want)
+        assert not got[rows:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_weight_gradient_of_groups_that_are_not_finite(tlc, fmt, dtype):
+    """A group with scale byte 255 makes its columns of dw NaN, whatever dy is there; the others are as without it.
+    The small tile, in one part and in slices, and the large one."""
+    for rows, n, cols in ((70, 40, 100), (5000, 130, 260), (330, 4096, 4096)):
+        say(f"case weight_grad not finite {rows}x{n}x{cols} {dtype} format {fmt}")
+        x = torch.randint(-7, 8, (rows, cols), generator=gen(1)).float()
+        dy = torch.randint(-3, 4, (rows, n), generator=gen(2)).to(dtype).cuda()
+        want = tlc.ckpt8_weight_grad(dy, tlc.ckpt8_pack(x.cuda(), fmt))
+        nan = torch.zeros(cols, dtype=torch.bool)
+        for row, col, v in ((11, 50, math.inf), (rows - 1, cols - 1, math.nan), (40, 2, -math.inf)):
+            x[row, col] = v
+            nan[col // 32 * 32:col // 32 * 32 + 32] = True
+        c = tlc.ckpt8_pack(x.cuda(), fmt)
+        assert int((c.scales == 255).sum()) == 3
+        got = tlc.ckpt8_weight_grad(dy, c)
+        nan = nan.cuda()
+        assert torch.isnan(got[:, nan]).all()
+        assert torch.equal(got[:, ~nan], want[:, ~nan])
+
+
 # ---- more than one launch ---------------------------------------------------
 #
 # HIP refuses a launch of 2^32 threads; the elementwise calls give a thread two
