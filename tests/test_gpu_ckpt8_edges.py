@@ -64,6 +64,43 @@ def test_gelu_in_the_negative_tail_is_right_relative_to_its_value(tlc, dtype):
         assert ((got - y64).abs() <= half * 1.0001 + tail_bound(a) * y64.abs()).all(), "y in 8 bits"
 
 
+# P falls as e^-k: k = x^2/2 (gelu), -u (gelu_tanh), -x (silu).  An exponent of
+# at most 8 roundings moves it by 8k * 2^-24 of itself, and what else is done to
+# it is below 16 roundings; f' has two parts, and for x <= -3 their sum is at
+# least 1/1.6 of the larger.  Where P is below 2^-126 it may be 0: |x| <= 88
+# times that.
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("kind", [ref.GELU, ref.GELU_TANH, ref.SILU])
+def test_activations_in_the_negative_tail(tlc, kind, dtype):
+    low = {ref.GELU: -13.0, ref.GELU_TANH: -10.0, ref.SILU: -87.0}[kind]
+    x = torch.linspace(low, -3.0, 4096).to(dtype).view(-1, 32)
+    rows, cols = x.shape
+    floor = 2.0 ** -119 + LEAST[dtype]
+
+    def act(a):
+        """f and f' as ref.act has them, but without tanh's cancellation, and the exponent k."""
+        if kind != ref.GELU_TANH:
+            return (*ref.act(kind, a), a * a / 2 if kind == ref.GELU else -a)
+        k = 2 * math.sqrt(2 / math.pi)
+        u = k * (a + 0.044715 * a ** 3)
+        p, q = torch.sigmoid(u), torch.sigmoid(-u)
+        return a * p, p + a * p * q * k * (1 + 0.134145 * a * a), -u
+
+    for fmt in FORMATS:
+        say(f"case tail of {kind} {rows}x{cols} {dtype} format {fmt}")
+        y, c, _ = tlc.ckpt8_act(x.cuda(), kind, fmt)
+        want, _, k = act(x.double())
+        assert_close(y, want, (U[dtype] * 1.01 + (16 + 8 * k) * 2.0 ** -24) * want.abs() + floor, "y")
+        ones = tlc.ckpt8_pack(torch.ones(rows, cols, device="cuda"), fmt)
+        da, db, _ = tlc.ckpt8_act_grad(torch.ones_like(x).cuda(), kind, c, ones)
+        f, slope, k = act(ref.decode(*ref.encode(x.double(), fmt), fmt, cols))
+        off = (16 + 8 * k) * 2.0 ** -24
+        assert_close(db, f, (U[dtype] * 1.01 + off) * f.abs() + floor, "db")
+        assert_close(da, slope, (U[dtype] * 1.01 + 1.6 * off) * slope.abs() + floor, "da")
+
+
 def test_gelu_tanh_gradient_in_fp32_counts_roundings(tlc):
     """f' = p + x*u'*p*q with p and q the logistic function of u and -u, both without a cancellation: u (below 4
     roundings) moves p by p*q*|u| of them and p*q by as much of itself, and the products round a few times more.
