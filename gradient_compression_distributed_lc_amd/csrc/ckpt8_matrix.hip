@@ -109,6 +109,14 @@ __device__ __forceinline__ float column_scale(const void* p, uint32_t c) {
 // and the next ones are on their way in registers.  The block meets once a
 // step, before the last products, whose operands it has then read; these run
 // while the next stage's first operands are read.
+//
+// Both groups of a block take the same number of steps and so meet equally
+// often, but where the rows end one can be in the branch-free loop and the
+// other in the one with checks: they then wait at two barriers of the code.
+// That is sound here because the barrier counts a workgroup's wavefronts
+// whichever instruction they arrive by, a wavefront takes either loop as a
+// whole (group is uniform in it), and no group reads the other's stages before
+// the exchange of sums, which all reach together.
 template <int kTerms, int kTile, int kStep>
 struct __align__(16) Stage {
     uint16_t a[kTerms][kStep][kTile];
@@ -392,7 +400,11 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
         // An edge, or dw is added to: 32 rows through LDS, so that a lane has 16
         // bytes of a row and eight reads of dw under way.  (8x8192x8192: 65 us
         // directly and 77 so; added to, 422 by a loop of single values and 129
-        // so.)  Nothing reads the stages after the last meeting.
+        // so.)  Nothing reads the stages after the last meeting.  The registers
+        // this takes beside the large tile's sums send 32 of those through
+        // scratch, once a tile after the main loop: 16384x8192x8192 1.69 ms
+        // against 1.67 with the loop of single values, 64x4096x4096 20 us
+        // against 19.
         constexpr int kHere = kGroups == 1 ? 2 : 4;  // wavefronts in each array of stages
         static_assert(sizeof(stages0) >= kHere * 32 * kWave * sizeof(float), "their rows fit");
         const int w = group * 4 + wave;
@@ -501,14 +513,21 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
 }
 
 // The tile and into how many slices the rows are cut, by the least of an
-// estimate in microseconds.  Measured: 32 rows of a 256x256 tile take 0.8 us a
-// bfloat16 term of dy, of a 128x128 tile 0.32 us, one block a CU, and a tile's
-// beginning and end 14 and 5 us.  Slices fill the chip where the tiles do not
-// (or leave a last round mostly empty) and cost writing and reading their sums.
-// bf16, e4m3: 16384x4096x4096 takes 430 us in tiles of 256 and 580 in tiles of
-// 128, 4096x4096x1024 (64 tiles of 256 in 4 slices) 62 and 43, 2048x2048x2048
-// 47 and 27, 512x1024x4096 34 and 13; 8192x1024x1024 in tiles of 128 takes 94
-// in one slice and 32 in four.
+// estimate in microseconds.  Measured, one block a CU: 32 rows of a 256x256
+// tile take 0.82 us (bf16; 0.92 for int8), 1.66 (fp16) and 2.6 (fp32), of a
+// 128x128 tile 0.29 (0.32), 0.54 and 0.78: 0.8 and 0.32 a term of dy are within
+// a fifth.  A tile's beginning and end take 14 and 5 us.  Slices fill the chip
+// where the tiles do not (or leave a last round mostly empty) and cost writing
+// and reading their sums.  Tiles of 256 and of 128, e4m3, us:
+//                     bf16          fp16          fp32
+//   16384x4096x4096   440  587      856  1075     1340  1577
+//   1024x4096x4096    44   63       71   91       100   120
+//   300x4096x4096     28   41       37   47       47    57
+//   4096x4096x1024    59   44       84   75       113   103
+//   2048x2048x2048    45   28       60   43       74    56
+//   512x1024x4096     24   14       38   17       53    22
+// The estimate takes the faster one in all of them but fp32 4096x4096x1024.
+// 8192x1024x1024 in tiles of 128 takes 94 us in one slice and 32 in four.
 struct Shape {
     uint32_t tile, slices;
     uint64_t slice_rows, tiles_i, tiles_c;
@@ -584,9 +603,10 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
                         using W = decltype(w);
                         constexpr int F = decltype(f)::value;
                         p.first = (uint32_t)first;
-                        // 64 rows a step are faster in the small tile of one term (59 us instead of 69 for
-                        // 4096x4096x1024 int8 in one group), slower with more LDS in use (1142 -> 1525, fp16
-                        // 16384x4096x4096)
+                        // The small tile with one term: 64 rows a step, with more 32, whose two groups' stages
+                        // of 64 would need 192 KB of LDS.  bf16 int8 with 64 and with 32: 4096x4096x1024 48.3 and
+                        // 49.4 us, 2048x2048x2048 29.2 and 29.9, 8192x1024x1024 33.5 and 34.1, 512x1024x4096 14.8
+                        // and 14.2.
                         if (s.tile == 256)
                             k_weight_grad<T, W, F, 256, 32, 1><<<blocks, threads, 0, st>>>(p);
                         else

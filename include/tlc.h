@@ -443,8 +443,13 @@ int tlc_planes_scatter(const float* src, const uint64_t* src_off, float* dst, co
  * stride (in elements, >= cols) apart, at any element: no alignment beyond the
  * element's is asked.  rows may be 0 (the call then writes nothing, except
  * where said otherwise); 1 <= cols and rows, cols, strides <= 2^31 - 1.
- * dtypes are enum tlc_dtype.  Arithmetic is fp32 or wider; each output is
- * rounded once, to nearest even.  Outputs must not overlap inputs or each
+ * dtypes are enum tlc_dtype.  Arithmetic is fp32 or wider, and each output is
+ * rounded to its type once, to nearest even.  What fp32 itself leaves open:
+ * f and the two parts of f' are within (16 + 8k)*2^-24 of their value, e^-k
+ * being what they fall as for negative x (k = x^2/2 for gelu), and may be 0
+ * where e^-k is below 2^-126; near x = 0 and for positive x k is 0.  y of the
+ * norm comes from 64 bits in fp32, and from rstd in fp32 in 16 bits (3*2^-24
+ * beside the type's rounding).  Outputs must not overlap inputs or each
  * other unless said otherwise.  No call here has a status word: nothing in the
  * data can be refused.  Workspaces as above (device, 256-byte aligned, size
  * from the *_workspace_size call, host only, 0 for sizes out of range). */
