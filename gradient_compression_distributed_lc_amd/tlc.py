@@ -756,6 +756,10 @@ def planes_scatter(src: torch.Tensor, src_off: torch.Tensor, dst: torch.Tensor, 
 # so halves of a fused projection need no copy).  The calls run on the device
 # of their tensors and on `stream`, or that device's current stream; buffers
 # that are not passed are allocated there, for that stream.
+#
+# Autograd does not see these calls: inputs may require a gradient, and results
+# are outside the graph.  The gradients are calls of their own, for a backward
+# pass that is written out or the methods of a torch.autograd.Function.
 
 CKPT8_INT8 = 1  # two's complement codes, -127..127
 CKPT8_E4M3 = 2  # 8-bit floats of 4 exponent and 3 fraction bits
@@ -931,7 +935,8 @@ def ckpt8_unpack(c: Checkpoint8, dtype: torch.dtype = torch.bfloat16, *, y: torc
 def ckpt8_act(a: torch.Tensor, act: int, fmt: int, b: torch.Tensor | None = None, *, y: torch.Tensor | None = None,
               a_out: Checkpoint8 | None = None, b_out: Checkpoint8 | None = None, stream=None):
     """y = f(a), or f(a)*b, with the checkpoints of a and b in the same pass.
-    Returns (y, checkpoint of a, checkpoint of b or None)."""
+    Returns (y, checkpoint of a, checkpoint of b or None), outside autograd's
+    graph: the gradient is ckpt8_act_grad."""
     pa, sa = _matrix(a, "a")
     _format(fmt)
     pb, sb = _matrix(b, "b", a) if b is not None else (None, 0)
@@ -986,7 +991,8 @@ def ckpt8_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float, fmt: in
     """Root-mean-square norm of x + residual.  Returns (sum, y, checkpoint,
     rstd): sum is x itself without a residual, y is None with want_y False, the
     checkpoint (of the normalised values, or with `weighted` of them times the
-    weight) is None with fmt None."""
+    weight) is None with fmt None.  All are outside autograd's graph: the
+    gradient is ckpt8_norm_grad."""
     px, sx = _matrix(x, "x")
     rows, cols = x.shape
     device = x.device
