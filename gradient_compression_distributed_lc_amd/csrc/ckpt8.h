@@ -59,7 +59,7 @@ struct Raw8 {
 // 8 or 0.  kNt: nontemporally.  Measured: reads of what the call alone needs
 // gain by it (32768x4096 bf16 packed in 64 us instead of 68, 16384x4096 gelu
 // gradient 53 instead of 58); the activation's and the norm's inputs, which the
-// kernel before has just written, do not (4096x4096 gelu 17.2 us instead of
+// kernel before has just written, do not (4096x4096 gelu 16.5 us instead of
 // 15.4).
 template <typename T, bool kNt = false>
 __device__ __forceinline__ Raw8<T> load8(const typename T::Elem* p, int n, bool whole = false) {
@@ -132,7 +132,7 @@ __device__ __forceinline__ Raw8<T> pack8(const float* v) {
 }
 
 // Results are written once and not read again here: nontemporally (4096x4096
-// bf16 gelu 17.2 -> 15.4 us, 16384x4096 norm 111 -> 105).
+// bf16 gelu 17.4 -> 15.4 us, 16384x4096 norm 112 -> 100).
 template <typename T>
 __device__ __forceinline__ void store8(typename T::Elem* p, int n, const Raw8<T>& r) {
     if (n >= 8) {

@@ -516,7 +516,7 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
 // estimate in microseconds.  Measured, one block a CU: 32 rows of a 256x256
 // tile take 0.82 us (bf16; 0.92 for int8), 1.66 (fp16) and 2.6 (fp32), of a
 // 128x128 tile 0.29 (0.32), 0.54 and 0.78: 0.8 and 0.32 a term of dy are within
-// a fifth.  A tile's beginning and end take 14 and 5 us.  Slices fill the chip
+// a quarter.  A tile's beginning and end take 14 and 5 us.  Slices fill the chip
 // where the tiles do not (or leave a last round mostly empty) and cost writing
 // and reading their sums.  Tiles of 256 and of 128, e4m3, us:
 //                     bf16          fp16          fp32
