@@ -16,7 +16,8 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "tlc.hip")
-SOURCES = [SRC, os.path.join(PKG, "csrc", "ckpt8.hip"), os.path.join(PKG, "csrc", "ckpt8_matrix.hip")]
+SOURCES = [SRC, os.path.join(PKG, "csrc", "ckpt8.hip"), os.path.join(PKG, "csrc", "ckpt8_matrix.hip"),
+           os.path.join(PKG, "csrc", "q8.hip"), os.path.join(PKG, "csrc", "products.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libtlc.so")

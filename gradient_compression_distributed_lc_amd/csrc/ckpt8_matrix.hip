@@ -1,5 +1,6 @@
 // ckpt8_matrix.hip -- the weight gradient from an 8-bit checkpoint:
 //   dw[i][c] (+)= col_scale[c] * sum over rows t of dy[t][i] * x[t][c],
+// over all rows or, for a weight of each expert, over the expert's own;
 // x the checkpoint's values.  x is a bfloat16 number as it stands, dy is one
 // (bf16), the sum of two (fp16) or of three (fp32) of them, so every product is
 // exact and the sums are the matrix cores' fp32.
@@ -8,11 +9,14 @@
 #include <cmath>
 
 #include "ckpt8.h"
+#include "experts.h"
 #include "launch.h"
 
 namespace {
 
 using namespace tlc_ckpt8;
+using tlc_experts::Experts;
+using tlc_experts::Span;
 using tlc_internal::launch_blocks;
 
 constexpr int kThreads = 256;  // of a group: four wavefronts, two by two
@@ -37,6 +41,10 @@ struct MatArgs {
     uint64_t slice_rows; // rows of one slice, a multiple of 64
     uint32_t tiles, tiles_i, tiles_c;  // tiles of dw, its rows of them, and those of one row
     uint32_t first;      // block of the whole that the launch begins with
+    // a weight for each expert
+    Experts experts;
+    uint64_t dw_expert;  // values between the experts' dw
+    uint32_t slices, tiles_all;  // slices of each expert's rows; tiles of all experts
 };
 
 // Place in the matrix of tile number `tile`: neighbours in bands of 4 rows of tiles.
@@ -156,7 +164,7 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <typename T, typename W, int FMT, int kTile, int kStep, int kGroups>
+template <typename T, typename W, int FMT, int kTile, int kStep, int kGroups, bool kExperts>
 __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p) {
     using Elem = typename T::Elem;
     constexpr int kTerms = T::kTerms;
@@ -174,14 +182,26 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
     // neighbouring tiles on one XCD: blocks go round the 8 of them
     uint32_t b = blockIdx.x;
     const uint32_t total = gridDim.x, per = total / 8;
-    if (b < per * 8) b = b % 8 * per + b / 8;
+    if constexpr (kExperts)
+        b = tlc_experts::xcd_place(b, total);
+    else if (b < per * 8)
+        b = b % 8 * per + b / 8;
     b += p.first;
-    const uint32_t slice = b / p.tiles, tile = b % p.tiles;
+    const uint32_t slice = b / (kExperts ? p.tiles_all : p.tiles), tile = b % p.tiles;
+    const uint32_t expert = kExperts ? b % p.tiles_all / p.tiles : 0;
     uint32_t tile_i, tile_c;
     tile_place(p, tile, &tile_i, &tile_c);
     const uint32_t i0 = tile_i * kTile, c0 = tile_c * kTile;
+    float* const dw = kExperts ? p.dw + expert * p.dw_expert : p.dw;
     // the group's share of the slice's rows, the same steps for each group
-    const uint64_t s_begin = slice * p.slice_rows, s_end = min(p.rows, s_begin + p.slice_rows);
+    uint64_t s_begin, s_end;
+    if constexpr (kExperts) {
+        const Span mine = tlc_experts::rows_of(p.experts, expert);
+        const uint64_t cut = ((mine.end - mine.begin + p.slices - 1) / p.slices + 63) / 64 * 64;
+        s_begin = min(mine.begin + slice * cut, (uint64_t)mine.end), s_end = min(s_begin + cut, (uint64_t)mine.end);
+    } else {
+        s_begin = slice * p.slice_rows, s_end = min(p.rows, s_begin + p.slice_rows);
+    }
     const uint64_t share = ((s_end - s_begin + kGroups - 1) / kGroups + kStep - 1) / kStep * kStep;
     const uint64_t t_begin = min(s_begin + group * share, s_end), t_end = min(t_begin + share, s_end);
     const int steps = (int)(share / kStep);
@@ -390,7 +410,7 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
             return;
         }
         if (direct) {
-            float* const o = p.dw + (i0 + wi + i * 32 + (lane >> 5) * 4) * p.dw_stride + col0;
+            float* const o = dw + (i0 + wi + i * 32 + (lane >> 5) * 4) * p.dw_stride + col0;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -426,21 +446,21 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
                 const uint32_t e = ((q + u) * 64 + lane) * 4, r = r0 + e / kWave, c = w0 + e % kWave;
                 old[u] = f4{0.0f, 0.0f, 0.0f, 0.0f};
                 if (p.accumulate && r < p.n && c + 4 <= p.cols)
-                    old[u] = *reinterpret_cast<const f4_at4*>(p.dw + r * p.dw_stride + c);
+                    old[u] = *reinterpret_cast<const f4_at4*>(dw + r * p.dw_stride + c);
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const uint32_t e = ((q + u) * 64 + lane) * 4, r = r0 + e / kWave, c = w0 + e % kWave;
                 const f4 s = *reinterpret_cast<const f4*>(mine + e);
                 if (r < p.n && c + 4 <= p.cols)
-                    *reinterpret_cast<f4_at4*>(p.dw + r * p.dw_stride + c) = p.accumulate ? old[u] + s : s;
+                    *reinterpret_cast<f4_at4*>(dw + r * p.dw_stride + c) = p.accumulate ? old[u] + s : s;
             }
         }
         // the last one to three columns of the matrix, a row a lane
         const uint32_t last = p.cols & ~3u;
         if (lane < 32 && last >= w0 && last < w0 + kWave && r0 + lane < p.n)
             for (uint32_t c = last; c < p.cols; ++c) {
-                float* const o = p.dw + (r0 + lane) * p.dw_stride + c;
+                float* const o = dw + (r0 + lane) * p.dw_stride + c;
                 const float s = mine[lane * kWave + c - w0];
                 *o = p.accumulate ? *o + s : s;
             }
@@ -484,7 +504,7 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
     const uint32_t b = p.first + blockIdx.x;
     const uint32_t tile = b / (per / kThreads), v = b % (per / kThreads) * kThreads + threadIdx.x;
     const f4* const in = p.partial + (uint64_t)tile * per + v;
-    const uint64_t next = (uint64_t)p.tiles * per;
+    const uint64_t next = (uint64_t)p.tiles_all * per;
     f4 s = {};
     uint32_t k = 0;
     for (; k + 4 <= slices; k += 4) {
@@ -496,7 +516,8 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
     }
     for (; k < slices; ++k) s += in[k * next];
     uint32_t ti, tc;
-    tile_place(p, tile, &ti, &tc);
+    tile_place(p, tile % p.tiles, &ti, &tc);
+    float* const dw = p.dw + (uint64_t)(tile / p.tiles) * p.dw_expert;
     // the lane's place in the product: wavefront, 32x32 part, four rows of one column
     const uint32_t parts = tile_size / 64, lane = v % 64, part = v / 256 % (parts * parts), wave = v / (per / 4);
     const uint32_t row = ti * tile_size + (wave >> 1) * (tile_size / 2) + part / parts * 32 + v / 64 % 4 * 8 +
@@ -507,7 +528,7 @@ __global__ __launch_bounds__(kThreads) void k_weight_sum(MatArgs p, uint32_t sli
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (row + j < p.n) {
-            float* const o = p.dw + (row + j) * p.dw_stride + col;
+            float* const o = dw + (row + j) * p.dw_stride + col;
             *o = p.accumulate ? *o + s[j] * cs : s[j] * cs;
         }
 }
@@ -532,7 +553,10 @@ struct Shape {
     uint32_t tile, slices;
     uint64_t slice_rows, tiles_i, tiles_c;
 };
-Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms) {
+// For a weight of each expert: every expert's rows are cut into as many
+// slices, and the estimate takes them as equally many.
+Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms, uint64_t experts = 1) {
+    rows = (rows + experts - 1) / experts;
     Shape best = {};
     double least = 0.0;
     for (uint32_t tile = 128; tile <= 256; tile *= 2) {
@@ -540,18 +564,66 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t cols, int terms) {
         for (uint64_t k : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
             if (k > 1 && rows / k < 128) break;
             const uint64_t cut = ((rows + k - 1) / k + 63) / 64 * 64, slices = cut ? (rows + cut - 1) / cut : 0;
-            const double blocks = (double)ti * (double)tc * (double)slices;
+            const double blocks = (double)ti * (double)tc * (double)slices * (double)experts;
             double us = std::ceil(blocks / 256) *
                         (tile == 256 ? 14.0 + 0.8 * terms * (double)(cut / 32) : 5.0 + 0.32 * terms * (double)(cut / 32));
-            if (slices > 1) us += 4.0 + (2.0 * slices + 1.0) * (double)n * (double)cols * 4.0 / 5.5e6;
+            if (slices > 1) us += 4.0 + (2.0 * slices + 1.0) * (double)n * (double)cols * (double)experts * 4.0 / 5.5e6;
             if (!best.tile || us < least) best = {tile, (uint32_t)slices, cut, ti, tc}, least = us;
         }
     }
     return best;
 }
 
-uint64_t workspace_of(const Shape& s) {
-    return s.slices > 1 ? s.slices * s.tiles_i * s.tiles_c * s.tile * s.tile * sizeof(float) : 256;
+uint64_t workspace_of(const Shape& s, uint64_t experts = 1) {
+    return s.slices > 1 ? s.slices * experts * s.tiles_i * s.tiles_c * s.tile * s.tile * sizeof(float) : 256;
+}
+
+// The launches of either call, p filled but for what the shape decides.
+template <bool kExperts>
+int weight_grad(MatArgs p, const Shape& s, int dtype, int col_scale_dtype, int format, void* workspace,
+                hipStream_t st) {
+    p.partial = s.slices > 1 ? static_cast<f4*>(workspace) : nullptr;
+    p.slice_rows = s.slice_rows, p.slices = s.slices;
+    p.tiles = (uint32_t)(s.tiles_i * s.tiles_c);
+    p.tiles_i = (uint32_t)s.tiles_i, p.tiles_c = (uint32_t)s.tiles_c;
+    p.tiles_all = kExperts ? p.tiles * p.experts.count : p.tiles;
+    const void* const col_scale = p.col_scale;
+    if (s.slices) {
+        const uint64_t all = (uint64_t)p.tiles_all * s.slices;
+        const uint32_t threads = s.tile == 256 ? kThreads : 2 * kThreads;
+        const char* const name = kExperts ? "tlc_expert_weight_grad" : "tlc_ckpt8_weight_grad";
+        const int rc = with_dtype(dtype, [&](auto t) {
+            return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
+                return with_format(format, [&](auto f) {
+                    return launch_blocks(name, st, all, threads, [&](uint64_t first, uint32_t blocks) {
+                        using T = decltype(t);
+                        using W = decltype(w);
+                        constexpr int F = decltype(f)::value;
+                        p.first = (uint32_t)first;
+                        // The small tile with one term: 64 rows a step, with more 32, whose two groups' stages
+                        // of 64 would need 192 KB of LDS.  bf16 int8 with 64 and with 32: 4096x4096x1024 48.3 and
+                        // 49.4 us, 2048x2048x2048 29.2 and 29.9, 8192x1024x1024 33.5 and 34.1, 512x1024x4096 14.8
+                        // and 14.2.
+                        if (s.tile == 256)
+                            k_weight_grad<T, W, F, 256, 32, 1, kExperts><<<blocks, threads, 0, st>>>(p);
+                        else
+                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32, 2, kExperts>
+                                <<<blocks, threads, 0, st>>>(p);
+                    });
+                });
+            });
+        });
+        if (rc || s.slices == 1) return rc;
+    }
+    const uint64_t all = (uint64_t)p.tiles_all * (s.tile * s.tile / 4 / kThreads);
+    return with_dtype(dtype, [&](auto t) {
+        return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
+            return launch_blocks("tlc_ckpt8_weight_sum", st, all, kThreads, [&](uint64_t first, uint32_t blocks) {
+                p.first = (uint32_t)first;
+                k_weight_sum<decltype(w)><<<blocks, kThreads, 0, st>>>(p, s.slices, s.tile);
+            });
+        });
+    });
 }
 
 }  // namespace
@@ -580,52 +652,51 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
     const Shape s = shape_of(rows, n, cols, dtype == TLC_F32 ? 3 : dtype == TLC_F16 ? 2 : 1);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_of(s)) return TLC_ERR_WORKSPACE;
     if (rows == 0 && accumulate) return TLC_OK;
-    MatArgs p;
+    MatArgs p = {};
     p.dy = dy, p.dy_stride = dy_stride, p.codes = codes, p.scales = scales, p.rows = rows;
     p.n = (uint32_t)n, p.cols = (uint32_t)cols;
     p.code_row = (uint32_t)code_stride(cols), p.scale_row = (uint32_t)scale_stride(cols);
     p.col_scale = col_scale;
     p.dw = dw, p.dw_stride = dw_stride, p.accumulate = accumulate != 0;
-    p.partial = s.slices > 1 ? static_cast<f4*>(workspace) : nullptr;
-    p.slice_rows = s.slice_rows;
-    p.tiles = (uint32_t)(s.tiles_i * s.tiles_c);
-    p.tiles_i = (uint32_t)s.tiles_i, p.tiles_c = (uint32_t)s.tiles_c;
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (s.slices) {
-        const uint64_t all = (uint64_t)p.tiles * s.slices;
-        const uint32_t threads = s.tile == 256 ? kThreads : 2 * kThreads;
-        const int rc = with_dtype(dtype, [&](auto t) {
-            return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
-                return with_format(format, [&](auto f) {
-                    return launch_blocks("tlc_ckpt8_weight_grad", st, all, threads, [&](uint64_t first,
-                                                                                         uint32_t blocks) {
-                        using T = decltype(t);
-                        using W = decltype(w);
-                        constexpr int F = decltype(f)::value;
-                        p.first = (uint32_t)first;
-                        // The small tile with one term: 64 rows a step, with more 32, whose two groups' stages
-                        // of 64 would need 192 KB of LDS.  bf16 int8 with 64 and with 32: 4096x4096x1024 48.3 and
-                        // 49.4 us, 2048x2048x2048 29.2 and 29.9, 8192x1024x1024 33.5 and 34.1, 512x1024x4096 14.8
-                        // and 14.2.
-                        if (s.tile == 256)
-                            k_weight_grad<T, W, F, 256, 32, 1><<<blocks, threads, 0, st>>>(p);
-                        else
-                            k_weight_grad<T, W, F, 128, T::kTerms == 1 ? 64 : 32, 2><<<blocks, threads, 0, st>>>(p);
-                    });
-                });
-            });
-        });
-        if (rc || s.slices == 1) return rc;
-    }
-    const uint64_t all = (uint64_t)p.tiles * (s.tile * s.tile / 4 / kThreads);
-    return with_dtype(dtype, [&](auto t) {
-        return with_weight(t, col_scale, col_scale_dtype, [&](auto w) {
-            return launch_blocks("tlc_ckpt8_weight_sum", st, all, kThreads, [&](uint64_t first, uint32_t blocks) {
-                p.first = (uint32_t)first;
-                k_weight_sum<decltype(w)><<<blocks, kThreads, 0, st>>>(p, s.slices, s.tile);
-            });
-        });
-    });
+    return weight_grad<false>(p, s, dtype, col_scale_dtype, format, workspace, static_cast<hipStream_t>(stream));
+}
+
+size_t tlc_expert_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols, uint64_t experts) {
+    if (!valid_shape(rows, cols) || n < 1 || n > kMaxDim || experts < 1 || experts > tlc_experts::kMaxExperts) return 0;
+    uint64_t bytes = 0;
+    for (int terms = 1; terms <= 3; ++terms)  // of any dtype
+        bytes = std::max(bytes, workspace_of(shape_of(rows, n, cols, terms, experts), experts));
+    return bytes;
+}
+
+int tlc_expert_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
+                           const uint8_t* codes, const uint8_t* scales, uint64_t cols, const uint64_t* offsets,
+                           uint64_t experts, const void* col_scale, int col_scale_dtype, float* dw, uint64_t dw_stride,
+                           uint64_t dw_expert_stride, int accumulate, void* workspace, size_t workspace_bytes,
+                           tlc_stream_t stream) {
+    if (!valid_dtype(dtype) || !valid_format(format) || !valid_shape(rows, cols) || n < 1 || n > kMaxDim ||
+        !valid_matrix(dw, TLC_F32, cols, dw_stride) || experts < 1 || experts > tlc_experts::kMaxExperts)
+        return TLC_ERR_INVALID_ARG;
+    if (offsets ? !aligned(offsets, 8) : experts != 1) return TLC_ERR_INVALID_ARG;
+    if (dw_expert_stride >> 48 || (experts > 1 && dw_expert_stride < (n - 1) * dw_stride + cols))
+        return TLC_ERR_INVALID_ARG;
+    if (rows && (!valid_matrix(dy, dtype, n, dy_stride) || !valid_checkpoint(codes, scales)))
+        return TLC_ERR_INVALID_ARG;
+    if (!valid_weight(col_scale, col_scale_dtype, dtype)) return TLC_ERR_INVALID_ARG;
+    if (((n + 127) / 128) * ((cols + 127) / 128) * experts > (1u << 24)) return TLC_ERR_INVALID_ARG;
+    const Shape s = shape_of(rows, n, cols, dtype == TLC_F32 ? 3 : dtype == TLC_F16 ? 2 : 1, experts);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < workspace_of(s, experts))
+        return TLC_ERR_WORKSPACE;
+    if (rows == 0 && accumulate) return TLC_OK;
+    MatArgs p = {};
+    p.dy = dy, p.dy_stride = dy_stride, p.codes = codes, p.scales = scales, p.rows = rows;
+    p.n = (uint32_t)n, p.cols = (uint32_t)cols;
+    p.code_row = (uint32_t)code_stride(cols), p.scale_row = (uint32_t)scale_stride(cols);
+    p.col_scale = col_scale;
+    p.dw = dw, p.dw_stride = dw_stride, p.accumulate = accumulate != 0;
+    p.experts = {offsets, (uint32_t)experts, (uint32_t)rows};
+    p.dw_expert = dw_expert_stride;
+    return weight_grad<true>(p, s, dtype, col_scale_dtype, format, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

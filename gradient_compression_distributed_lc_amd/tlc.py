@@ -104,6 +104,19 @@ _SIGS = {
                                  _I, _P, _SZ, _P]),
     "tlc_ckpt8_weight_grad_workspace_size": (_SZ, [_U64, _U64, _U64]),
     "tlc_ckpt8_weight_grad": (_I, [_P, _U64, _I, _U64, _U64, _I, _P, _P, _U64, _P, _I, _P, _U64, _I, _P, _SZ, _P]),
+    "tlc_q8_code_stride": (_U64, [_U64]),
+    "tlc_q8_pack_rows": (_I, [_P, _U64, _I, _U64, _U64, _P, _P, _P]),
+    "tlc_q8_pack_columns_workspace_size": (_SZ, [_U64, _U64]),
+    "tlc_q8_pack_columns": (_I, [_P, _U64, _I, _U64, _U64, _P, _P, _P, _SZ, _P]),
+    "tlc_q8_product_workspace_size": (_SZ, [_U64, _U64, _U64, _U64]),
+    "tlc_q8_product": (_I, [_P, _P, _U64, _P, _P, _U64, _U64, _P, _U64, _P, _U64, _I, _I, _P, _SZ, _P]),
+    "tlc_expert_product_workspace_size": (_SZ, [_U64, _U64, _U64, _U64, _I]),
+    "tlc_expert_product": (_I, [_P, _U64, _I, _U64, _U64, _P, _U64, _U64, _U64, _P, _U64, _P, _U64, _P, _SZ, _P]),
+    "tlc_expert_input_grad_workspace_size": (_SZ, [_U64, _U64, _U64, _U64, _I]),
+    "tlc_expert_input_grad": (_I, [_P, _U64, _I, _U64, _U64, _P, _U64, _U64, _U64, _P, _U64, _P, _U64, _P, _SZ, _P]),
+    "tlc_expert_weight_grad_workspace_size": (_SZ, [_U64, _U64, _U64, _U64]),
+    "tlc_expert_weight_grad": (_I, [_P, _U64, _I, _U64, _U64, _I, _P, _P, _U64, _P, _U64, _P, _I, _P, _U64, _U64, _I,
+                                    _P, _SZ, _P]),
     "tlc_profile_enable": (_I, [_I]),
     "tlc_profile_read": (_I, [ctypes.POINTER(KernelTime), _I, ctypes.POINTER(_I)]),
     "tlc_profile_only": (_I, [ctypes.c_char_p]),
@@ -1091,6 +1104,257 @@ def ckpt8_weight_grad(dy: torch.Tensor, x: Checkpoint8, *, col_scale: torch.Tens
         _check(lib().tlc_ckpt8_weight_grad(pd, sd, _DTYPES[dy.dtype], rows, n, x.format, pc, ps, cols, pcs, cdt, pg,
                                            sg, int(accumulate), ws.data_ptr(), ws.numel(), st),
                "tlc_ckpt8_weight_grad")
+        return g
+    return _on_stream(device, stream, body)
+
+
+# ---- 8-bit integers with a scale per row, products grouped by expert ---------
+#
+# These calls know nothing of autograd either: see the note above.
+
+
+@dataclass
+class Rows8:
+    """A matrix [rows, cols] in 8-bit integers with one scale per row (layout in
+    tlc.h): value [r, c] is codes[r, c] * scales[r], codes past cols are 0.
+    Rows can be sliced off as ``Rows8(q.codes[a:b], q.scales[a:b], q.cols)``."""
+    codes: torch.Tensor   # int8[rows, 128*ceil(cols/128)]
+    scales: torch.Tensor  # float32[rows]
+    cols: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def q8_code_stride(cols: int) -> int:
+    return int(lib().tlc_q8_code_stride(cols))
+
+
+def _rows8(q: Rows8, name: str, rows: int, cols: int, device):
+    """(codes pointer, scales pointer) of a matrix [rows, cols] in 8-bit integers."""
+    if q.cols != cols:
+        raise ValueError(f"{name} must hold {cols} columns, got {q.cols}")
+    shape = (rows, -(-cols // 128) * 128)
+    t = q.codes
+    if t.shape != shape or t.dtype != torch.int8 or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}.codes must be contiguous int8{list(shape)} on a GPU, {device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr(), _vector(q.scales, rows, device, f"{name}.scales", torch.float32)[0]
+
+
+def _rows8_for(out: Rows8 | None, rows: int, cols: int, device):
+    """(matrix, codes pointer, scales pointer): `out`, checked, or a new one."""
+    if out is not None:
+        return (out, *_rows8(out, "out", rows, cols, device))
+    codes = torch.empty((rows, -(-cols // 128) * 128), dtype=torch.int8, device=device)
+    scales = torch.empty(rows, dtype=torch.float32, device=device)
+    return Rows8(codes, scales, cols), codes.data_ptr(), scales.data_ptr()
+
+
+def _offsets(offsets: torch.Tensor | None, experts: int, device):
+    """Pointer of the experts' row offsets, None for None (one expert with every row)."""
+    if offsets is None:
+        if experts != 1:
+            raise ValueError(f"offsets are needed for {experts} experts")
+        return None
+    if offsets.dtype != torch.int64 or offsets.device != device or not offsets.is_contiguous() \
+            or offsets.dim() != 1 or offsets.shape[0] != experts + 1:
+        raise ValueError(f"offsets must be contiguous int64[{experts + 1}] on {device}, got "
+                         f"{tuple(offsets.shape)} of {offsets.dtype} on {offsets.device}")
+    return offsets.data_ptr()
+
+
+def _weights(w: torch.Tensor, like: torch.Tensor):
+    """(pointer, row stride, expert stride) of weights [experts, rows, columns]."""
+    if w.dim() != 3 or w.shape[0] < 1 or w.shape[1] < 1 or w.shape[2] < 1:
+        raise ValueError(f"w must be [experts, rows, columns], each at least 1, got shape {tuple(w.shape)}")
+    if w.dtype != like.dtype or w.device != like.device:
+        raise ValueError(f"w must be of {like.dtype} on {like.device}, got {w.dtype} on {w.device}")
+    _, rows, cols = w.shape
+    expert, row, col = w.stride()
+    if col != 1 and cols != 1 or row < cols and rows > 1:
+        raise ValueError(f"w must have adjacent columns and rows that do not overlap, got strides {w.stride()}")
+    return w.data_ptr(), row if rows > 1 else cols, expert
+
+
+def _result(out: torch.Tensor | None, name: str, rows: int, cols: int, dtype: torch.dtype, device):
+    """(matrix, pointer, row stride): `out`, checked, or a new one."""
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        return out, out.data_ptr(), cols
+    p, stride = _matrix(out, name)
+    if out.shape[0] != rows or out.shape[1] != cols or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{name} must be ({rows}, {cols}) of {dtype} on {device}, got {tuple(out.shape)} of "
+                         f"{out.dtype} on {out.device}")
+    return out, p, stride
+
+
+def _product_workspace(nbytes: int, device, workspace):
+    """(pointer, bytes) of a workspace that may need nothing."""
+    if nbytes == 0 and workspace is None:
+        return None, 0
+    ws = _ckpt8_workspace(nbytes, device, workspace)
+    return ws.data_ptr(), ws.numel()
+
+
+def q8_pack_rows(x: torch.Tensor, *, out: Rows8 | None = None, stream=None) -> Rows8:
+    """The rows of a matrix in 8-bit integers, a scale each: tokens of an
+    activation, output channels of a weight."""
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+
+    def body(st):
+        q, pc, ps = _rows8_for(out, rows, cols, x.device)
+        _check(lib().tlc_q8_pack_rows(px, sx, _DTYPES[x.dtype], rows, cols, pc, ps, st), "tlc_q8_pack_rows")
+        return q
+    return _on_stream(x.device, stream, body)
+
+
+@functools.lru_cache(maxsize=1024)
+def q8_pack_columns_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().tlc_q8_pack_columns_workspace_size(rows, cols))
+
+
+def q8_pack_columns(x: torch.Tensor, *, out: Rows8 | None = None, workspace=None, stream=None) -> Rows8:
+    """The columns of a matrix [rows, cols] in 8-bit integers, a scale each, as
+    the matrix [cols, rows]."""
+    px, sx = _matrix(x, "x")
+    rows, cols = x.shape
+
+    def body(st):
+        q, pc, ps = _rows8_for(out, cols, rows, x.device)
+        ws = _ckpt8_workspace(q8_pack_columns_workspace_size(rows, cols), x.device, workspace)
+        _check(lib().tlc_q8_pack_columns(px, sx, _DTYPES[x.dtype], rows, cols, pc, ps, ws.data_ptr(), ws.numel(), st),
+               "tlc_q8_pack_columns")
+        return q
+    return _on_stream(x.device, stream, body)
+
+
+@functools.lru_cache(maxsize=1024)
+def q8_product_workspace_size(rows: int, n: int, k: int, experts: int = 1) -> int:
+    return int(lib().tlc_q8_product_workspace_size(rows, n, k, experts))
+
+
+def q8_product(a: Rows8, w: Rows8, dtype: torch.dtype = torch.bfloat16, *, offsets: torch.Tensor | None = None,
+               y: torch.Tensor | None = None, accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
+    """y[a.rows, n] = a w^T of `dtype`, both in 8-bit integers; n is w.rows, or
+    with offsets (int64[experts + 1], the rows of each expert) w.rows / experts.
+    Rows of no expert are not written.  With `accumulate` added to y (float32)."""
+    rows, k, device = a.rows, a.cols, a.codes.device
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    experts = offsets.shape[0] - 1 if offsets is not None and offsets.dim() == 1 else 1
+    if experts < 1 or w.rows < 1 or w.rows % experts:
+        raise ValueError(f"w must have the same number of rows for each of {experts} experts, got {w.rows}")
+    if accumulate and (y is None or dtype != torch.float32):
+        raise ValueError("accumulate needs y, float32")
+    n = w.rows // experts
+    pa, psa = _rows8(a, "a", rows, k, device)
+    pw, psw = _rows8(w, "w", w.rows, k, device)
+    po = _offsets(offsets, experts, device)
+
+    def body(st):
+        o, py, sy = _result(y, "y", rows, n, dtype, device)
+        pws, nws = _product_workspace(q8_product_workspace_size(rows, n, k, experts), device, workspace)
+        _check(lib().tlc_q8_product(pa, psa, rows, pw, psw, n, k, po, experts, py, sy, _DTYPES[dtype],
+                                    int(accumulate), pws, nws, st), "tlc_q8_product")
+        return o
+    return _on_stream(device, stream, body)
+
+
+@functools.lru_cache(maxsize=1024)
+def expert_product_workspace_size(rows: int, k: int, n: int, experts: int, dtype: torch.dtype) -> int:
+    return int(lib().tlc_expert_product_workspace_size(rows, k, n, experts, _DTYPES[dtype]))
+
+
+def expert_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None, *,
+                   y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """y[rows, n]: each row of x[rows, k] times its expert's weight transposed,
+    w[experts, n, k].  offsets: int64[experts + 1] on the device, expert e has
+    rows offsets[e] .. offsets[e+1]-1 (None: one expert with every row).  Rows
+    of no expert are not written."""
+    px, sx = _matrix(x, "x")
+    pw, sw, se = _weights(w, x)
+    rows, k = x.shape
+    experts, n, wk = w.shape
+    device = x.device
+    if wk != k:
+        raise ValueError(f"w must have {k} columns, got {wk}")
+    pf = _offsets(offsets, experts, device)
+
+    def body(st):
+        o, py, sy = _result(y, "y", rows, n, x.dtype, device)
+        pws, nws = _product_workspace(expert_product_workspace_size(rows, k, n, experts, x.dtype), device, workspace)
+        _check(lib().tlc_expert_product(px, sx, _DTYPES[x.dtype], rows, k, pw, sw, se, n, pf, experts, py, sy, pws,
+                                        nws, st), "tlc_expert_product")
+        return o
+    return _on_stream(device, stream, body)
+
+
+@functools.lru_cache(maxsize=1024)
+def expert_input_grad_workspace_size(rows: int, n: int, k: int, experts: int, dtype: torch.dtype) -> int:
+    return int(lib().tlc_expert_input_grad_workspace_size(rows, n, k, experts, _DTYPES[dtype]))
+
+
+def expert_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None, *,
+                      dx: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """dx[rows, k], the gradient of expert_product by x: each row of dy[rows, n]
+    times its expert's weight.  Rows of no expert are not written."""
+    pd, sd = _matrix(dy, "dy")
+    pw, sw, se = _weights(w, dy)
+    rows, n = dy.shape
+    experts, wn, k = w.shape
+    device = dy.device
+    if wn != n:
+        raise ValueError(f"w must have {n} rows for each expert, got {wn}")
+    pf = _offsets(offsets, experts, device)
+
+    def body(st):
+        o, po, so = _result(dx, "dx", rows, k, dy.dtype, device)
+        pws, nws = _product_workspace(expert_input_grad_workspace_size(rows, n, k, experts, dy.dtype), device,
+                                      workspace)
+        _check(lib().tlc_expert_input_grad(pd, sd, _DTYPES[dy.dtype], rows, n, pw, sw, se, k, pf, experts, po, so, pws,
+                                           nws, st), "tlc_expert_input_grad")
+        return o
+    return _on_stream(device, stream, body)
+
+
+@functools.lru_cache(maxsize=1024)
+def expert_weight_grad_workspace_size(rows: int, n: int, cols: int, experts: int) -> int:
+    return int(lib().tlc_expert_weight_grad_workspace_size(rows, n, cols, experts))
+
+
+def expert_weight_grad(dy: torch.Tensor, x: Checkpoint8, offsets: torch.Tensor | None = None, *,
+                       col_scale: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                       accumulate: bool = False, workspace=None, stream=None) -> torch.Tensor:
+    """dw[experts, n, cols] (float32), the gradient of expert_product by w with
+    x kept as an 8-bit checkpoint: for each expert dy^T x over its rows (times
+    col_scale per column).  With `accumulate` added to dw, which may be a view
+    into a flat gradient buffer."""
+    pd, sd = _matrix(dy, "dy")
+    rows, n = dy.shape
+    cols, device = x.cols, dy.device
+    pc, ps = _checkpoint(x, "x", rows, cols, device)
+    pcs, cdt = _vector(col_scale, cols, device, "col_scale")
+    experts = offsets.shape[0] - 1 if offsets is not None and offsets.dim() == 1 else 1
+    if experts < 1:
+        raise ValueError("offsets must have at least two entries")
+    pf = _offsets(offsets, experts, device)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+
+    def body(st):
+        g = dw if dw is not None else torch.empty((experts, n, cols), dtype=torch.float32, device=device)
+        if g.shape != (experts, n, cols) or g.dtype != torch.float32 or g.device != device:
+            raise ValueError(f"dw must be ({experts}, {n}, {cols}) of float32 on {device}")
+        pg, sg, se = _weights(g, g)
+        if experts > 1 and se < (n - 1) * sg + cols:
+            raise ValueError(f"dw must have experts that do not overlap, got strides {g.stride()}")
+        ws = _ckpt8_workspace(expert_weight_grad_workspace_size(rows, n, cols, experts), device, workspace)
+        _check(lib().tlc_expert_weight_grad(pd, sd, _DTYPES[dy.dtype], rows, n, x.format, pc, ps, cols, pf, experts,
+                                            pcs, cdt, pg, sg, se, int(accumulate), ws.data_ptr(), ws.numel(), st),
+               "tlc_expert_weight_grad")
         return g
     return _on_stream(device, stream, body)
 

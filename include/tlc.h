@@ -540,6 +540,93 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
                           int col_scale_dtype, float* dw, uint64_t dw_stride, int accumulate, void* workspace,
                           size_t workspace_bytes, tlc_stream_t stream);
 
+/* ---- 8-bit integers with a scale per row, and their product -----------------
+ * A matrix [rows, cols] in 8-bit integers has one fp32 scale per row: per token
+ * for activations, per output channel for a weight [channels, inputs].
+ *   codes   int8[rows][tlc_q8_code_stride(cols)], 16-byte aligned;
+ *   scales  float[rows].
+ * Codes past a row's columns are written as 0, and the product reads them.
+ * With amax the row's largest magnitude, the scale is amax/127 and a code is
+ * the nearest integer to x * (127/amax), ties to even, both quotients rounded
+ * to fp32; where amax < 127*2^-126 the scale is 2^-126 and 127/amax is 2^126.
+ * A value is code*scale.  A row with an infinity or a NaN has codes 0 and scale
+ * NaN.  The three products of a linear layer y = x W^T are products of such
+ * matrices:
+ *   y  = x W^T:    rows of x     by rows of W;
+ *   dx = dy W:     rows of dy    by columns of W;
+ *   dW = dy^T x:   columns of dy by columns of x, fp32, into a gradient bucket.
+ * Strides, dtypes, sizes and refusals as for the checkpoints above, and
+ * cols <= 131072, so that sums of products stay in 32 bits. */
+
+/* Bytes between the rows of codes: a multiple of 128.  0 for cols out of range. */
+uint64_t tlc_q8_code_stride(uint64_t cols);
+
+/* The rows of x[rows, cols].  rows may be 0. */
+int tlc_q8_pack_rows(const void* x, uint64_t x_stride, int dtype, uint64_t rows, uint64_t cols, int8_t* codes,
+                     float* scales, tlc_stream_t stream);
+
+/* The columns of x[rows, cols]: codes int8[cols][tlc_q8_code_stride(rows)] and
+ * scales float[cols], as tlc_q8_pack_rows would make them of x transposed.
+ * 1 <= rows <= 131072. */
+size_t tlc_q8_pack_columns_workspace_size(uint64_t rows, uint64_t cols);
+int tlc_q8_pack_columns(const void* x, uint64_t x_stride, int dtype, uint64_t rows, uint64_t cols, int8_t* codes,
+                        float* scales, void* workspace, size_t workspace_bytes, tlc_stream_t stream);
+
+/* y[t][o] = a_scales[t] * w_scales[o] * sum over c < k of a[t][c]*w[o][c]
+ * (added to y[t][o] with accumulate != 0, fp32 only), a [rows, k] and w [n, k]
+ * as above.  The sum is exact; its conversion to fp32 and the two products with
+ * the scales, the smaller one first, are rounded, and the result is rounded to
+ * y's dtype.  With offsets, rows are grouped by expert (below) and w holds
+ * experts*n rows, expert e's from e*n.
+ * The workspace may be NULL where the size is 0. */
+size_t tlc_q8_product_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts);
+int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const int8_t* w, const float* w_scales,
+                   uint64_t n, uint64_t k, const uint64_t* offsets, uint64_t experts, void* y, uint64_t y_stride,
+                   int dtype, int accumulate, void* workspace, size_t workspace_bytes, tlc_stream_t stream);
+
+/* ---- products grouped by expert ---------------------------------------------
+ * The rows of a layer split over experts lie expert by expert: expert e has
+ * rows offsets[e] .. offsets[e+1]-1, none to all of them.  offsets is a device
+ * array of experts+1 entries, 8-byte aligned, which the kernels read: no host
+ * synchronisation.  An entry above `rows` counts as `rows` and one below an
+ * earlier entry as that one; rows of no expert are not read and their results
+ * are left as they were.  1 <= experts <= 65536.  offsets may be NULL with one
+ * expert, which then has every row.
+ * w is [experts][n][k], its rows w_stride and its experts w_expert_stride
+ * elements apart (0 included: the same weight for all).  Matrices of one call
+ * have one dtype; sums are fp32 in a fixed order and rounded to the dtype once.
+ * Outputs must not overlap inputs.  Strides, sizes and refusals as for the
+ * checkpoints above; TLC_ERR_INVALID_ARG also for more than 2^24 tiles of
+ * 128 x 128 (rows/128 + experts of them in the rows).  The workspace may be
+ * NULL where the size is 0. */
+
+/* y[t][o] = sum over c of x[t][c] * w[e][o][c], e the expert of row t. */
+size_t tlc_expert_product_workspace_size(uint64_t rows, uint64_t k, uint64_t n, uint64_t experts, int dtype);
+int tlc_expert_product(const void* x, uint64_t x_stride, int dtype, uint64_t rows, uint64_t k, const void* w,
+                       uint64_t w_stride, uint64_t w_expert_stride, uint64_t n, const uint64_t* offsets,
+                       uint64_t experts, void* y, uint64_t y_stride, void* workspace, size_t workspace_bytes,
+                       tlc_stream_t stream);
+
+/* Its gradient by x: dx[t][c] = sum over o of dy[t][o] * w[e][o][c]. */
+size_t tlc_expert_input_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int dtype);
+int tlc_expert_input_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, const void* w,
+                          uint64_t w_stride, uint64_t w_expert_stride, uint64_t k, const uint64_t* offsets,
+                          uint64_t experts, void* dx, uint64_t dx_stride, void* workspace, size_t workspace_bytes,
+                          tlc_stream_t stream);
+
+/* Its gradient by w, x being kept as an 8-bit checkpoint:
+ *   dw[e][i][c] = col_scale[c] * sum over the expert's rows t of dy[t][i]*x[t][c]
+ * (added to with accumulate != 0); everything else as tlc_ckpt8_weight_grad.
+ * dw is fp32 [experts][n][cols], rows dw_stride and experts dw_expert_stride
+ * >= (n-1)*dw_stride + cols values apart.  An expert without rows gets 0, or
+ * keeps its dw with accumulate. */
+size_t tlc_expert_weight_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t cols, uint64_t experts);
+int tlc_expert_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_t rows, uint64_t n, int format,
+                           const uint8_t* codes, const uint8_t* scales, uint64_t cols, const uint64_t* offsets,
+                           uint64_t experts, const void* col_scale, int col_scale_dtype, float* dw, uint64_t dw_stride,
+                           uint64_t dw_expert_stride, int accumulate, void* workspace, size_t workspace_bytes,
+                           tlc_stream_t stream);
+
 /* ---- measurement helpers (not part of the codec) -------------------------- */
 
 /* Streaming copy of `bytes` bytes (a multiple of 16, both pointers 16-byte
