@@ -6,6 +6,7 @@
 // row of either side.  16-bit and fp32 sums are the matrix cores' fp32, integer
 // sums are exact in 32 bits.
 #include <algorithm>
+#include <numeric>
 #include <type_traits>
 
 #include "ckpt8.h"
@@ -40,6 +41,8 @@ struct ProductArgs {
     void* y;
     uint64_t y_stride;
     int accumulate;
+    uint32_t* partial;                      // with several slices: their sums, [slices][rows][partial_row]
+    uint32_t partial_row, slices, slice_k;  // n up to a multiple of 8; a slice's share of k, whole steps
     uint32_t tiles_n;
     uint32_t first;                         // block of the whole that the launch begins with
 };
@@ -72,21 +75,36 @@ __device__ __forceinline__ typename Sums<E>::Type multiply(u4 a, u4 b, typename 
     }
 }
 
-// The first n of the elements in 16 bytes at p, the rest 0.
-template <typename E>
-__device__ __forceinline__ u4 load16(const typename E::Elem* p, int n) {
-    if constexpr (sizeof(typename E::Elem) == 2) {
-        return load8<E>(p, n).w[0];
-    } else if constexpr (sizeof(typename E::Elem) == 4) {
-        if (n >= 4) return *reinterpret_cast<const u4_at4*>(p);
-        u4 r = {};
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (j < n) r[j] = reinterpret_cast<const uint32_t*>(p)[j];
-        return r;
-    } else {
-        return *reinterpret_cast<const u4*>(p);  // codes are padded with zeros
-    }
+template <typename Elem>
+__device__ __forceinline__ const Elem* later(const Elem* p, uint32_t bytes) {
+    return reinterpret_cast<const Elem*>(reinterpret_cast<const char*>(p) + bytes);
+}
+
+// Sixteen bytes at any element's boundary.
+template <typename Elem>
+__device__ __forceinline__ u4 load16(const Elem* p) {
+    if constexpr (sizeof(Elem) == 1)
+        return *reinterpret_cast<const u4*>(p);  // codes are aligned
+    else if constexpr (sizeof(Elem) == 2)
+        return *reinterpret_cast<const u4_at2*>(p);
+    else
+        return *reinterpret_cast<const u4_at4*>(p);
+}
+
+// Elements first .. of a row of `limit` elements, at least sixteen bytes long:
+// what lies past the row is 0.  A chunk that the row ends in is read from the
+// row's last sixteen bytes and moved.
+template <typename Elem>
+__device__ __forceinline__ u4 load16_cut(const Elem* row, uint32_t first, uint32_t limit) {
+    const uint32_t at = min(first, limit - (uint32_t)(16 / sizeof(Elem)));
+    const u4 v = load16(row + at);
+    const uint32_t s = min((first - at) * 8 * (uint32_t)sizeof(Elem), 128u);
+    uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    if (s >= 64) lo = hi, hi = 0;
+    const uint32_t t = s & 63;
+    if (t) lo = lo >> t | hi << (64 - t), hi >>= t;
+    if (s >= 128) lo = 0;
+    return u4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // The scales' product with a sum: the smaller scale first, so that nothing
@@ -106,22 +124,53 @@ __device__ __forceinline__ s4v read_tr(const void* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p);
 }
 
+// The order of instructions among kProducts products, each of which keeps the
+// matrix core busy for 32 clocks: LDS reads, LDS writes and loads, each kind
+// spread evenly over them.
+template <int kProducts, int kReads, int kWrites, int kLoads>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+        for (int r = i * kReads / kProducts; r < (i + 1) * kReads / kProducts; ++r)
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+        for (int r = i * kWrites / kProducts; r < (i + 1) * kWrites / kProducts; ++r)
+            __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+#pragma unroll
+        for (int r = i * kLoads / kProducts; r < (i + 1) * kLoads / kProducts; ++r)
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+}
+
 // A block computes kTile x kTile values of y, each of its four wavefronts a
 // quarter, in steps of 128 bytes of the reduction.
+//
+// Two stages of LDS.  While one is multiplied, the step loaded before goes to
+// the other, and as its registers are freed the step after is loaded into them:
+// a load has a whole step's products to arrive in.  The block meets once a step,
+// before the last quarter of the products, whose operands it has then read;
+// these run while the next stage's first operands are read.
 template <typename E, typename Out, bool kInner, int kTile>
-__global__ __launch_bounds__(kThreads, 2) void k_product(ProductArgs p) {
+__global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(ProductArgs p) {
     using Elem = typename E::Elem;
     using Acc = typename Sums<E>::Type;
-    constexpr int kPer = 16 / sizeof(Elem);     // elements of a 16-byte chunk
-    constexpr int kStep = 128 / sizeof(Elem);   // of the reduction in a step
+    constexpr int kPer = 16 / sizeof(Elem);       // elements of a 16-byte chunk
+    constexpr int kStep = 128 / sizeof(Elem);     // of the reduction in a step
     constexpr int kLoads = kTile * 8 / kThreads;  // chunks a lane, of either operand
     constexpr int kWave = kTile / 2, kTiles = kWave / 32;
-    __shared__ u4 stages[2][2][kTile * 8];
+    struct Stage {
+        u4 a[kTile * 8], w[kTile * 8];
+    };
+    __shared__ Stage stage0, stage1;
 
     uint32_t b = p.first + blockIdx.x;
-    const uint32_t tiles_t = tiles_of(p.experts, kTile), total = tiles_t * p.tiles_n;
+    const uint32_t tiles_t = tiles_of(p.experts, kTile), tiles = tiles_t * p.tiles_n, total = tiles * p.slices;
     if (b >= total) return;
     b = xcd_place(b, total);
+    const uint32_t slice = p.slices > 1 ? b / tiles : 0;
+    b -= slice * tiles;
     // bands of 4 tiles of rows
     const uint32_t band = b / (4 * p.tiles_n), in_band = b % (4 * p.tiles_n);
     const uint32_t band_rows = min(4u, tiles_t - band * 4);
@@ -129,41 +178,79 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductArgs p) {
     const uint32_t o0 = in_band / band_rows * kTile;
     if (at.begin >= at.end) return;  // offsets that change meanwhile
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const Elem* const a = static_cast<const Elem*>(p.a);
-    const Elem* const w = static_cast<const Elem*>(p.w) + at.expert * p.w_expert;
-    const int steps = (int)((p.k + kStep - 1) / kStep);
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const uint32_t k_first = slice * p.slice_k, k_here = min(p.k - k_first, p.slice_k);
+    const Elem* const a = static_cast<const Elem*>(p.a) + at.begin * p.a_stride + k_first;
+    const Elem* const w = static_cast<const Elem*>(p.w) + at.expert * p.w_expert +
+                          (kInner ? k_first : o0) * p.w_stride + (kInner ? 0 : k_first);
+    const int steps = (int)((k_here + kStep - 1) / kStep);
+    // Steps whose every chunk can be read as it lies.  A chunk past the inner
+    // weight's last column runs on into the next row, so not in the last row;
+    // columns past the last one only reach values that are not stored.
+    const int whole = (int)((k_here - (kInner && p.n % kPer ? 1 : 0)) / kStep);
 
-    // Rows of 128 bytes: slot c of row r holds chunk c ^ (r/2 % 8).
-    const int row = tid / 8, chunk = tid % 8 ^ (row >> 1 & 7);
+    // Rows of 128 bytes: slot c of row r holds chunk c ^ (r/2 % 8), so that the
+    // 16 rows that lanes read at once fall into all 64 banks.  The inner weight's
+    // rows are the reduction and kTile columns long: see operand_columns.
+    const int row = tid / 8, chunk = tid % 8;
+    const int place_a = row * 8 + (chunk ^ (row >> 1 & 7));
+    const uint32_t last_a = at.end - at.begin - 1, last_w = p.n - 1 - o0;
+    constexpr int kChunks = kTile / kPer;  // of a row of the inner weight
+    constexpr int kInnerRows = kThreads / kChunks;
+    static_assert(kInnerRows % 4 == 0, "a lane's rows have one swizzle");
+    const int inner_row = tid / kChunks;
+    const int inner_chunk = tid % kChunks;
+    const int place_w = !kInner              ? place_a
+                        : sizeof(Elem) == 2 ? inner_row * kChunks + (inner_chunk ^ ((inner_row & 3) << 2 | (inner_row & 1)))
+                                            : tid;
+    const uint32_t inner_col = o0 + inner_chunk * kPer;
+
+    uint32_t from_a[kLoads], from_w[kInner ? 1 : kLoads];  // bytes
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        from_a[i] = min((uint32_t)row + i * 32, last_a) * (uint32_t)(p.a_stride * sizeof(Elem)) + chunk * 16;
+    if constexpr (kInner) {
+        from_w[0] = inner_row * (uint32_t)(p.w_stride * sizeof(Elem)) +
+                    (inner_col < p.n ? inner_col : 0) * (uint32_t)sizeof(Elem);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            from_w[i] = min((uint32_t)row + i * 32, last_w) * (uint32_t)(p.w_stride * sizeof(Elem)) + chunk * 16;
+    }
     u4 ga[kLoads], gw[kLoads];
-    auto load = [&](int s) {
-        const int left = (int)p.k - s * kStep - chunk * kPer;
-        const uint64_t at_k = (uint64_t)s * kStep + (left > 0 ? chunk * kPer : 0);
+    // The first or the last chunks of a whole step.
+    constexpr int kEarly = kLoads * 3 / 4;
+    auto load_whole = [&](int s, int from, int to) {
+        const Elem* const pa = a + (uint64_t)s * kStep;
+        const Elem* const pw = w + (uint64_t)s * kStep * (kInner ? p.w_stride : 1);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t r = min(at.begin + row + i * 32, at.end - 1);
-            ga[i] = left > 0 ? load16<E>(a + r * p.a_stride + at_k, left) : u4{0, 0, 0, 0};
+        for (int i = from; i < to; ++i) {
+            ga[i] = load16(later(pa, from_a[i]));
+            gw[i] = load16(kInner ? later(pw + i * kInnerRows * p.w_stride, from_w[0])
+                                  : later(pw, from_w[kInner ? 0 : i]));
         }
+    };
+    auto load = [&](int s) {
+        if (s < whole) return load_whole(s, 0, kLoads);
+        // in the whole row, which has sixteen bytes where a slice's end may not
+        const uint32_t k0 = k_first + s * kStep + chunk * kPer;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
+            ga[i] = load16_cut(later(a - k_first, from_a[i] - chunk * 16), k0, p.k);
             if constexpr (!kInner) {
-                const uint32_t r = min(o0 + row + i * 32, p.n - 1);
-                gw[i] = left > 0 ? load16<E>(w + r * p.w_stride + at_k, left) : u4{0, 0, 0, 0};
+                gw[i] = load16_cut(later(w - k_first, from_w[i] - chunk * 16), k0, p.k);
             } else {
-                constexpr int kChunks = kTile / kPer;  // of a row of the weight
-                const uint32_t id = i * kThreads + tid, r = id / kChunks;
-                const uint32_t c = sizeof(Elem) == 2 ? id % kChunks ^ ((r & 3) << 2 | (r & 1)) : id % kChunks;
-                const uint32_t o = s * kStep + r, col = o0 + c * kPer;
-                gw[i] = o < p.k && col < p.n ? load16<E>(w + o * p.w_stride + col, (int)(p.n - col)) : u4{0, 0, 0, 0};
+                const uint32_t o = s * kStep + inner_row + i * kInnerRows;
+                gw[i] = load16_cut(w + min(o, k_here - 1) * p.w_stride, inner_col, p.n);
+                if (o >= k_here) gw[i] = u4{0, 0, 0, 0};
             }
         }
     };
-    auto store = [&](int s) {
+    auto store = [&](Stage& st) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            stages[s & 1][0][i * kThreads + tid] = ga[i];
-            stages[s & 1][1][i * kThreads + tid] = gw[i];
+            st.a[i * kThreads + place_a] = ga[i];
+            st.w[i * kThreads + place_w] = gw[i];
         }
     };
 
@@ -173,11 +260,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductArgs p) {
     auto operand_rows = [&](const u4* st, int sub, int from) {  // of 32 rows beginning with `from`
         return st[(from + r32) * 8 + ((sub * 2 + half) ^ (r32 >> 1 & 7))];
     };
+    // Columns of rows of the reduction.  16 bits: the transposing read gives
+    // each of 16 lanes 4 rows of one column from 4 rows of 16 columns; the
+    // 16-byte slots (8 columns) of row r lie at slot ^ (r%4*4 | r%2), so that
+    // the 4 rows x 32 columns read at once fall into the 64 banks once each.
     auto operand_columns = [&](const u4* st, int sub, int from) {
         if constexpr (sizeof(Elem) == 2) {
-            const int r = sub * 16 + half * 8 + (lane >> 2 & 3);
+            const int r = half * 8 + (lane >> 2 & 3);
             const int slot = from / 8 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
-            const char* q = reinterpret_cast<const char*>(st) + r * kTile * 2 +
+            const char* q = reinterpret_cast<const char*>(st) + (sub * 16 + r) * kTile * 2 +
                             (slot ^ ((r & 3) << 2 | (r & 1))) * 16 + (lane & 1) * 8;
             const s4v lo = read_tr(q), hi = read_tr(q + 4 * kTile * 2);
             return __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -186,106 +277,325 @@ __global__ __launch_bounds__(kThreads, 2) void k_product(ProductArgs p) {
             return u4{q[0], q[kTile], q[2 * kTile], q[3 * kTile]};
         }
     };
-    if (steps > 0) {
-        load(0);
-        store(0);
+    u4 fa[2][kTiles], fw[2][kTiles];
+    auto operands = [&](const Stage& st, int sub) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+            fw[sub & 1][i] = kInner ? operand_columns(st.w, sub, wc + i * 32) : operand_rows(st.w, sub, wc + i * 32);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) fa[sub & 1][i] = operand_rows(st.a, sub, wi + i * 32);
+    };
+    auto products = [&](const u4* ra, const u4* rw) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E>(ra[i], rw[c], acc[i][c]);
+    };
+    constexpr bool kSchedule = sizeof(Elem) <= 2;
+    constexpr int kProducts = kTiles * kTiles, kReads = kTiles * (kInner ? 3 : 2);  // of a quarter, 16 bits or 8
+    // Step s multiplies `now`, stores step s + 1 to `next` and loads step s + 2.
+    // kMain: all of it, of whole steps, without a branch, so that one schedule
+    // spans it.
+    auto step = [&](Stage& now, Stage& next, int s, auto main) {
+        constexpr bool kMain = decltype(main)::value;
+        if (!kMain && s + 1 >= 0 && s + 1 < steps) store(next);
+        if (!kMain && s + 2 < steps) load(s + 2);
+        if (kMain || s >= 0) {
+#pragma unroll
+            for (int sub = 0; sub < 3; ++sub) {
+                operands(now, sub + 1);
+                products(fa[sub & 1], fw[sub & 1]);
+            }
+        }
+        if constexpr (kMain) {
+            store(next);
+            load_whole(s + 2, 0, kEarly);
+            if constexpr (kSchedule) interleave<3 * kProducts, 3 * kReads, 2 * kLoads, 2 * kEarly>();
+        }
+        __syncthreads();
+        u4 la[kTiles], lw[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) la[i] = fa[1][i], lw[i] = fw[1][i];
+        if (kMain || (s + 1 >= 0 && s + 1 < steps)) operands(next, 0);
+        if (kMain || s >= 0) products(la, lw);
+        if constexpr (kMain) {
+            load_whole(s + 2, kEarly, kLoads);
+            if constexpr (kSchedule) interleave<kProducts, kReads, 0, 2 * (kLoads - kEarly)>();
+        }
+    };
+    // The steps before 0 fill the pipeline.
+    for (int s = -2; s < steps; ++s) {
+        if (s >= 0 && s % 2 == 0)
+            for (; s + 3 < whole; s += 2) {
+                step(stage0, stage1, s, Int<1>{});
+                step(stage1, stage0, s + 1, Int<1>{});
+            }
+        step(s & 1 ? stage1 : stage0, s & 1 ? stage0 : stage1, s, Int<0>{});
     }
     __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) load(s + 1);
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-            u4 fa[kTiles], fb[kTiles];
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                fa[i] = operand_rows(stages[s & 1][0], sub, wi + i * 32);
-                fb[i] = kInner ? operand_columns(stages[s & 1][1], sub, wc + i * 32)
-                               : operand_rows(stages[s & 1][1], sub, wc + i * 32);
-            }
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E>(fa[i], fb[c], acc[i][c]);
-        }
-        if (s + 1 < steps) store(s + 1);
-        __syncthreads();
-    }
 
     // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32.
-    // 32 rows at a time through LDS, so that a lane has eight values of a row.
-    uint32_t* const mine = reinterpret_cast<uint32_t*>(&stages[0][0][0]) + wave * 32 * kWave;
-    constexpr int kAcross = kWave / 8, kDown = 64 / kAcross;
+    // 64 rows at a time through LDS, so that a lane has eight values of a row.
+    // Short loops: code that runs once costs more to fetch than to run.
+    static_assert(2 * sizeof(Stage) >= 4 * 64 * kWave * sizeof(uint32_t), "the wavefronts' rows fit");
+    uint32_t* const mine = reinterpret_cast<uint32_t*>(wave < 2 ? &stage0 : &stage1) + wave % 2 * 64 * kWave;
+    constexpr int kAcross = kWave / 8, kDown = 64 / kAcross, kDeep = 4;
     const uint32_t col = o0 + wc + lane % kAcross * 8;
     const int count = (int)min((int64_t)p.n - (int64_t)col, (int64_t)8);
+    const bool add = std::is_same<E, I8>::value && std::is_same<Out, F32>::value && p.accumulate;
     float sw[8];
     if constexpr (std::is_same<E, I8>::value) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sw[j] = j < count ? p.w_scales[(uint64_t)at.expert * p.n + col + j] : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
+    for (int i = 0; i < kTiles; i += 2) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < 32; ++j)
 #pragma unroll
             for (int c = 0; c < kTiles; ++c) {
-                const auto v = acc[i][c][j];
-                mine[((j >> 2) * 8 + half * 4 + (j & 3)) * kWave + c * 32 + r32] = __builtin_bit_cast(uint32_t, v);
+                const auto v = acc[i + j / 16][c][j % 16];
+                mine[(j / 4 * 8 + half * 4 + j % 4) * kWave + c * 32 + r32] = __builtin_bit_cast(uint32_t, v);
             }
         wave_sync();
+        const uint32_t t0 = at.begin + wi + i * 32;
+#pragma unroll 1
+        for (int q = 0; q < 64 && t0 + q < at.end; q += kDown * kDeep) {
+            u4 in[kDeep][2];
+            float sa[kDeep];
 #pragma unroll
-        for (int q = 0; q < 32; q += kDown) {
-            const uint32_t r = q + lane / kAcross, t = at.begin + wi + i * 32 + r;
-            if (t < at.end && count > 0) {
-                const u4* const in = reinterpret_cast<const u4*>(mine + r * kWave + lane % kAcross * 8);
-                const u4 lo = in[0], hi = in[1];
+            for (int d = 0; d < kDeep; ++d) {
+                const uint32_t r = q + d * kDown + lane / kAcross;
+                const u4* const from = reinterpret_cast<const u4*>(mine + r * kWave + lane % kAcross * 8);
+                in[d][0] = from[0], in[d][1] = from[1];
+                if constexpr (std::is_same<E, I8>::value) sa[d] = p.a_scales[min(t0 + r, at.end - 1)];
+            }
+#pragma unroll
+            for (int d = 0; d < kDeep; ++d) {
+                const uint32_t t = t0 + q + d * kDown + lane / kAcross;
+                if (p.partial) {
+                    u4* const o = reinterpret_cast<u4*>(
+                        p.partial + ((uint64_t)slice * p.experts.rows + t) * p.partial_row + col);
+                    if (t < at.end && count > 0) o[0] = in[d][0], o[1] = in[d][1];
+                    continue;
+                }
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t u = j < 4 ? lo[j & 3] : hi[j & 3];
+                    const uint32_t u = in[d][j / 4][j % 4];
                     if constexpr (std::is_same<E, I8>::value)
-                        v[j] = scaled((int)u, p.a_scales[t], sw[j]);
+                        v[j] = scaled((int)u, sa[d], sw[j]);
                     else
                         v[j] = from_bits(u);
                 }
+                if (t >= at.end || count < 8) continue;
                 typename Out::Elem* const o = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + col;
-                if constexpr (std::is_same<Out, F32>::value) {
-                    if (p.accumulate) {
-                        float old[8];
-                        unpack8<Out>(load8<Out>(o, count), old);
+                if (add) {
+                    float old[8];
+                    unpack8<Out>(load8<Out>(o, 8, true), old);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] += old[j];
-                    }
+                    for (int j = 0; j < 8; ++j) v[j] += old[j];
                 }
-                store8<Out>(o, count, pack8<Out>(v));
+                store8<Out>(o, 8, pack8<Out>(v));
+            }
+        }
+        // the last one to seven columns of y, a row a lane
+        const uint32_t ragged = p.n & ~7u, t = t0 + lane;
+        if (!p.partial && ragged < p.n && ragged >= o0 + wc && ragged < o0 + wc + kWave && t < at.end) {
+#pragma unroll 1
+            for (uint32_t c = ragged; c < p.n; ++c) {
+                typename Out::Elem* const o = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + c;
+                const uint32_t u = mine[lane * kWave + c - (o0 + wc)];
+                float v;
+                if constexpr (std::is_same<E, I8>::value)
+                    v = scaled((int)u, p.a_scales[t], p.w_scales[(uint64_t)at.expert * p.n + c]);
+                else
+                    v = from_bits(u);
+                if (add) v += (float)*o;
+                *o = (typename Out::Elem)v;
             }
         }
         wave_sync();
     }
 }
 
+// y from the slices' sums, added in order: eight columns of a row a thread.
+template <typename E, typename Out>
+__global__ __launch_bounds__(kThreads) void k_product_sum(ProductArgs p) {
+    constexpr uint32_t kRows = 32, kAcross = kThreads / kRows;  // of a block
+    const uint32_t b = p.first + blockIdx.x, tile = b / p.tiles_n;
+    if (tile >= tiles_of(p.experts, kRows)) return;
+    const Span at = tile_rows(p.experts, kRows, tile);
+    const uint32_t t = at.begin + threadIdx.x / kAcross, col = (b % p.tiles_n * kAcross + threadIdx.x % kAcross) * 8;
+    if (t >= at.end || col >= p.n) return;
+    const uint32_t* const in = p.partial + (uint64_t)t * p.partial_row + col;
+    const uint64_t next = (uint64_t)p.experts.rows * p.partial_row;
+    typename std::conditional<std::is_same<E, I8>::value, int, float>::type sum[8] = {};
+#pragma unroll 4
+    for (uint32_t s = 0; s < p.slices; ++s) {
+        const u4 lo = *reinterpret_cast<const u4*>(in + s * next), hi = *reinterpret_cast<const u4*>(in + s * next + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t u = j < 4 ? lo[j & 3] : hi[j & 3];
+            if constexpr (std::is_same<E, I8>::value)
+                sum[j] += (int)u;
+            else
+                sum[j] += from_bits(u);
+        }
+    }
+    const int count = (int)min(p.n - col, 8u);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (std::is_same<E, I8>::value)
+            v[j] = j < count ? scaled(sum[j], p.a_scales[t], p.w_scales[(uint64_t)at.expert * p.n + col + j]) : 0.0f;
+        else
+            v[j] = sum[j];
+    }
+    typename Out::Elem* const o = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + col;
+    if (std::is_same<E, I8>::value && std::is_same<Out, F32>::value && p.accumulate) {
+        float old[8];
+        unpack8<Out>(load8<Out>(o, count), old);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += old[j];
+    }
+    store8<Out>(o, count, pack8<Out>(v));
+}
+
+// Rows of less than 16 bytes: a value a thread.
+template <typename Elem>
+bool narrow(uint64_t n, uint64_t k, bool inner) {
+    return std::min(k, inner ? n : k) < 16 / sizeof(Elem);
+}
+template <typename E, bool kInner>
+__global__ __launch_bounds__(kThreads) void k_product_narrow(ProductArgs p, uint64_t first) {
+    using Elem = typename E::Elem;
+    const uint64_t v = (first + blockIdx.x) * kThreads + threadIdx.x;
+    const uint32_t t = (uint32_t)(v / p.n), o = (uint32_t)(v % p.n);
+    // the expert: the last whose rows begin at or before t and do not end there
+    uint32_t expert = 0;
+    bool found = !p.experts.offsets;
+    if (p.experts.offsets) {
+        uint32_t before = 0;
+        for (uint32_t e = 0; e < p.experts.count && !found; ++e) {
+            const uint32_t begin = max(before, held(p.experts, e)), end = max(begin, held(p.experts, e + 1));
+            found = t >= begin && t < end;
+            expert = e, before = end;
+        }
+    }
+    if (t >= p.experts.rows || !found) return;
+    const Elem* const a = static_cast<const Elem*>(p.a) + t * p.a_stride;
+    const Elem* const w = static_cast<const Elem*>(p.w) + expert * p.w_expert + (kInner ? o : o * p.w_stride);
+    float sum = 0.0f;
+    for (uint32_t k = 0; k < p.k; ++k) sum = fmaf((float)a[k], (float)w[kInner ? k * p.w_stride : k], sum);
+    static_cast<Elem*>(p.y)[t * p.y_stride + o] = (Elem)sum;
+}
+
+// The tile and the slices of the reduction, by the least of an estimate in
+// microseconds.  Measured, in steps of 128 bytes: a 128x128 tile takes 0.5 us a
+// step alone on a CU, two at once 1.0, a 256x256 tile 1.55, in 16 bits and in 8
+// (fp32, in the smaller tile only: 2.0 and 4.6); a tile's beginning and end take
+// 4 and 8 us.  Slices fill the chip where the tiles do not and cost writing and
+// reading their sums.  Rows of experts are taken as equally many: half a tile
+// more for each.
+struct Shape {
+    uint32_t tile, slices, slice_k;
+};
+Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool grouped, int size) {
+    const uint64_t step = 128 / size, steps = (k + step - 1) / step;
+    Shape best = {};
+    double least = 0.0;
+    for (uint32_t tile = 128; tile <= (size == 4 ? 128 : 256); tile *= 2) {
+        const uint64_t worst = most_tiles(rows, experts, tile, grouped);
+        const double tiles_t = grouped ? std::min((double)worst, (double)rows / tile + 0.5 * (double)experts) : worst;
+        for (uint64_t slices : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+            if (slices > 1 && steps < 4 * slices) break;
+            const uint64_t share = (steps + slices - 1) / slices, cut = (steps + share - 1) / share;
+            if (worst * ((n + tile - 1) / tile) * cut > 0xFFFFFFFFull) break;
+            const double blocks = std::max(1.0, tiles_t * (double)((n + tile - 1) / tile) * (double)cut);
+            double us;
+            if (tile == 256) {
+                us = std::ceil(blocks / 256) * (1.55 * (double)share + 8.0);
+            } else {
+                const double one = (size == 4 ? 2.0 : 0.5) * (double)share, two = (size == 4 ? 4.6 : 1.0) * (double)share;
+                const double full = std::floor(blocks / 512), rest = blocks - full * 512;
+                us = full * (two + 4.0) + (rest <= 0.0 ? 0.0 : rest <= 256 ? one + 4.0 : two + 4.0);
+            }
+            if (cut > 1) us += 4.0 + (2.0 * (double)cut + 1.0) * (double)rows * (double)n * 4.0 / 5.5e6;
+            if (!best.tile || us < least) best = {tile, (uint32_t)cut, (uint32_t)(share * step)}, least = us;
+        }
+    }
+    return best;
+}
+
+uint64_t partial_row(uint64_t n) { return (n + 7) / 8 * 8; }
+uint64_t workspace_of(const Shape& s, uint64_t rows, uint64_t n) {
+    return s.slices > 1 ? (s.slices * rows * partial_row(n) * 4 + 255) / 256 * 256 : 0;
+}
+
 template <typename E, typename Out, bool kInner>
-int product(const char* name, ProductArgs p, hipStream_t st) {
-    const uint64_t tiles_t = most_tiles(p.experts.rows, p.experts.count, 128, p.experts.offsets != nullptr);
-    p.tiles_n = (p.n + 127) / 128;
-    return launch_blocks(name, st, tiles_t * p.tiles_n, kThreads, [&](uint64_t first, uint32_t blocks) {
+int product(const char* name, ProductArgs p, void* workspace, size_t workspace_bytes, hipStream_t st) {
+    using Elem = typename E::Elem;
+    const bool grouped = p.experts.offsets != nullptr;
+    if constexpr (!std::is_same<E, I8>::value) {
+        if (narrow<Elem>(p.n, p.k, kInner)) {
+            const uint64_t blocks = ((uint64_t)p.experts.rows * p.n + kThreads - 1) / kThreads;
+            return launch_blocks(name, st, blocks, kThreads, [&](uint64_t first, uint32_t here) {
+                k_product_narrow<E, kInner><<<here, kThreads, 0, st>>>(p, first);
+            });
+        }
+    }
+    const Shape s = shape_of(p.experts.rows, p.n, p.k, p.experts.count, grouped, sizeof(Elem));
+    const uint64_t need = workspace_of(s, p.experts.rows, p.n);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return TLC_ERR_WORKSPACE;
+    p.slices = s.slices, p.slice_k = s.slice_k, p.partial_row = (uint32_t)partial_row(p.n);
+    p.partial = s.slices > 1 ? static_cast<uint32_t*>(workspace) : nullptr;
+    auto go = [&](auto tile) {
+        constexpr int kTile = decltype(tile)::value;
+        p.tiles_n = (p.n + kTile - 1) / kTile;
+        const uint64_t tiles_t = most_tiles(p.experts.rows, p.experts.count, kTile, grouped);
+        return launch_blocks(name, st, tiles_t * p.tiles_n * s.slices, kThreads, [&](uint64_t first, uint32_t blocks) {
+            p.first = (uint32_t)first;
+            k_product<E, Out, kInner, kTile><<<blocks, kThreads, 0, st>>>(p);
+        });
+    };
+    int rc = TLC_OK;
+    if constexpr (sizeof(Elem) == 4)
+        rc = go(Int<128>{});
+    else
+        rc = s.tile == 256 ? go(Int<256>{}) : go(Int<128>{});
+    if (rc || s.slices == 1) return rc;
+    p.tiles_n = (p.partial_row / 8 + 7) / 8;
+    const uint64_t tiles_t = most_tiles(p.experts.rows, p.experts.count, 32, grouped);
+    return launch_blocks("tlc_product_sum", st, tiles_t * p.tiles_n, kThreads, [&](uint64_t first, uint32_t blocks) {
         p.first = (uint32_t)first;
-        k_product<E, Out, kInner, 128><<<blocks, kThreads, 0, st>>>(p);
+        k_product_sum<E, Out><<<blocks, kThreads, 0, st>>>(p);
     });
 }
 
-constexpr uint64_t kMaxTiles = 1u << 24;  // of 128 x 128
+constexpr uint64_t kMaxTiles = 1u << 24;   // of 128 x 128
+constexpr uint64_t kMaxStride = 1u << 22;  // a tile's 256 rows of fp32 lie within 32 bits
 
-bool valid_product(uint64_t rows, uint64_t n, uint64_t k, const void* offsets, uint64_t experts) {
-    if (!valid_shape(rows, n) || k < 1 || k > kMaxDim || experts < 1 || experts > kMaxExperts) return false;
-    if (offsets ? !aligned(offsets, 8) : experts != 1) return false;
-    return most_tiles(rows, experts, 128, offsets != nullptr) * ((n + 127) / 128) <= kMaxTiles;
+bool valid_product(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts) {
+    return valid_shape(rows, n) && k >= 1 && k <= kMaxDim && experts >= 1 && experts <= kMaxExperts &&
+           most_tiles(rows, experts, 128, true) * ((n + 127) / 128) <= kMaxTiles;
+}
+bool valid_offsets(const void* offsets, uint64_t experts) { return offsets ? aligned(offsets, 8) : experts == 1; }
+
+// Of one expert, with offsets and without: what either call may need.
+size_t product_workspace(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int size) {
+    if (rows < 1 || !valid_product(rows, n, k, experts)) return 0;
+    uint64_t bytes = workspace_of(shape_of(rows, n, k, experts, true, size), rows, n);
+    if (experts == 1) bytes = std::max(bytes, workspace_of(shape_of(rows, n, k, 1, false, size), rows, n));
+    return bytes;
 }
 
 int expert_call(const char* name, bool inner, const void* a, uint64_t a_stride, int dtype, uint64_t rows,
                 uint64_t k, const void* w, uint64_t w_stride, uint64_t w_expert_stride, uint64_t w_cols, uint64_t n,
-                const uint64_t* offsets, uint64_t experts, void* y, uint64_t y_stride, void*, size_t,
-                tlc_stream_t stream) {
-    if (!valid_dtype(dtype) || !valid_product(rows, n, k, offsets, experts) || w_expert_stride >> 48)
+                const uint64_t* offsets, uint64_t experts, void* y, uint64_t y_stride, void* workspace,
+                size_t workspace_bytes, tlc_stream_t stream) {
+    if (!valid_dtype(dtype) || !valid_product(rows, n, k, experts) || !valid_offsets(offsets, experts) || w_expert_stride >> 48 ||
+        a_stride > kMaxStride || w_stride > kMaxStride)
         return TLC_ERR_INVALID_ARG;
     if (rows == 0) return TLC_OK;
     if (!valid_matrix(a, dtype, k, a_stride) || !valid_matrix(w, dtype, w_cols, w_stride) ||
@@ -299,7 +609,8 @@ int expert_call(const char* name, bool inner, const void* a, uint64_t a_stride, 
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        return inner ? product<T, T, true>(name, p, st) : product<T, T, false>(name, p, st);
+        return inner ? product<T, T, true>(name, p, workspace, workspace_bytes, st)
+                     : product<T, T, false>(name, p, workspace, workspace_bytes, st);
     });
 }
 
@@ -307,15 +618,28 @@ int expert_call(const char* name, bool inner, const void* a, uint64_t a_stride, 
 
 extern "C" {
 
-size_t tlc_q8_product_workspace_size(uint64_t, uint64_t, uint64_t, uint64_t) { return 0; }
-size_t tlc_expert_product_workspace_size(uint64_t, uint64_t, uint64_t, uint64_t, int) { return 0; }
-size_t tlc_expert_input_grad_workspace_size(uint64_t, uint64_t, uint64_t, uint64_t, int) { return 0; }
+size_t tlc_q8_product_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts) {
+    const uint64_t stride = tlc_q8_code_stride(k);
+    return stride ? product_workspace(rows, n, stride, experts, 1) : 0;
+}
+
+size_t tlc_expert_product_workspace_size(uint64_t rows, uint64_t k, uint64_t n, uint64_t experts, int dtype) {
+    if (!valid_dtype(dtype)) return 0;
+    const int size = dtype == TLC_F32 ? 4 : 2;
+    return k < 16u / size ? 0 : product_workspace(rows, n, k, experts, size);
+}
+
+size_t tlc_expert_input_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int dtype) {
+    if (!valid_dtype(dtype)) return 0;
+    const int size = dtype == TLC_F32 ? 4 : 2;
+    return std::min(n, k) < 16u / size ? 0 : product_workspace(rows, k, n, experts, size);
+}
 
 int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const int8_t* w, const float* w_scales,
                    uint64_t n, uint64_t k, const uint64_t* offsets, uint64_t experts, void* y, uint64_t y_stride,
-                   int dtype, int accumulate, void*, size_t, tlc_stream_t stream) {
+                   int dtype, int accumulate, void* workspace, size_t workspace_bytes, tlc_stream_t stream) {
     const uint64_t stride = tlc_q8_code_stride(k);
-    if (!valid_dtype(dtype) || !stride || !valid_product(rows, n, k, offsets, experts) ||
+    if (!valid_dtype(dtype) || !stride || !valid_product(rows, n, k, experts) || !valid_offsets(offsets, experts) ||
         (accumulate && dtype != TLC_F32))
         return TLC_ERR_INVALID_ARG;
     if (rows == 0) return TLC_OK;
@@ -329,7 +653,8 @@ int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const 
     p.a_scales = a_scales, p.w_scales = w_scales;
     p.y = y, p.y_stride = y_stride, p.accumulate = accumulate != 0;
     return with_dtype(dtype, [&](auto t) {
-        return product<I8, decltype(t), false>("tlc_q8_product", p, static_cast<hipStream_t>(stream));
+        return product<I8, decltype(t), false>("tlc_q8_product", p, workspace, workspace_bytes,
+                                               static_cast<hipStream_t>(stream));
     });
 }
 

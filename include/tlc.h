@@ -597,7 +597,8 @@ int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const 
  * have one dtype; sums are fp32 in a fixed order and rounded to the dtype once.
  * Outputs must not overlap inputs.  Strides, sizes and refusals as for the
  * checkpoints above; TLC_ERR_INVALID_ARG also for more than 2^24 tiles of
- * 128 x 128 (rows/128 + experts of them in the rows).  The workspace may be
+ * 128 x 128 (rows/128 + experts of them in the rows) and, in the first two
+ * calls, for x_stride, dy_stride or w_stride above 2^22.  The workspace may be
  * NULL where the size is 0. */
 
 /* y[t][o] = sum over c of x[t][c] * w[e][o][c], e the expert of row t. */

@@ -303,6 +303,26 @@ def test_expert_products(tlc, rows, k, n, experts, dtype):
             assert_close(got[b:t], want, bound, (e, terms))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k", [1027, 2050, 4099, 8191])
+def test_long_reductions_of_few_rows(tlc, k, dtype):
+    """Few tiles and a long reduction, whose slices end at odd places: the last one may be shorter than 16 bytes."""
+    rows, n, counts = 40, 72, [25, 0, 15]
+    g = gen(k)
+    x, w = whole(g, rows, k, dtype=dtype, most=1), whole(g, 3, n, k, dtype=dtype, most=1)
+    off = offsets_of(counts).cuda()
+    y = tlc.expert_product(strided(x, 3, 1), strided(w, 1, 0), off)
+    # the same numbers as the reduction of the gradient: w transposed, its rows the reduction
+    z = tlc.expert_input_grad(x.cuda(), w.transpose(1, 2).contiguous().cuda(), off)
+    for e, (b, t) in enumerate(ref.spans(off.tolist(), rows)):
+        want = (x[b:t].double() @ w[e].double().t()).to(dtype)
+        assert torch.equal(y[b:t].cpu(), want) and torch.equal(z[b:t].cpu(), want), e
+    q = [random_codes(g, r, k) for r in (rows, 3 * n)]
+    y8 = tlc.q8_product(*[rows8(tlc, c, torch.ones(c.shape[0]), k) for c, _ in q], torch.float32, offsets=off)
+    for e, (b, t) in enumerate(ref.spans(off.tolist(), rows)):
+        assert torch.equal(y8[b:t].cpu(), (q[0][0][b:t].double() @ q[1][0][e * n:(e + 1) * n].double().t()).float())
+
+
 def test_offsets_that_are_not_in_order(tlc):
     """Offsets that fall, are negative or past the rows: held to the rows and to not falling, nothing else is written."""
     rows, k, n = 300, 96, 40
