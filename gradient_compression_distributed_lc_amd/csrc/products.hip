@@ -419,6 +419,112 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     }
 }
 
+// Few rows: a block computes 16x16 values of y, its eight wavefronts taking the
+// reduction in turns of 128 bytes.  Operands go from memory to the matrix cores
+// without LDS: w is read once in all, the few rows of a once for each block.
+// Two or four times the columns a block (so fewer reads of a), 4 or 16
+// wavefronts and 8 turns under way measured the same or slower (1x8192x4096
+// bf16 17.0 us with its launch; 16.8 to 28.3).  A row of 8192x4096 bf16, 67 MB,
+// takes about 11 us of its own, 16 rows of 8192x8192 40.
+template <typename E>
+struct FewSums {
+    using Type = f4;
+};
+template <>
+struct FewSums<I8> {
+    using Type = i4;
+};
+template <typename E>
+__device__ __forceinline__ typename FewSums<E>::Type multiply_few(u4 a, u4 b, typename FewSums<E>::Type c) {
+    if constexpr (std::is_same<E, I8>::value)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, a), __builtin_bit_cast(i4, b), c, 0, 0, 0);
+    else if constexpr (std::is_same<E, BF16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0,
+                                                       0);
+    else if constexpr (std::is_same<E, F16>::value)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0,
+                                                      0);
+    else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(from_bits(a[j]), from_bits(b[j]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+template <typename E, typename Out>
+__global__ __launch_bounds__(512) void k_product_few(ProductArgs p) {
+    constexpr int kWaves = 8, kDeep = 4;  // turns under way
+    using Elem = typename E::Elem;
+    using Acc = typename FewSums<E>::Type;
+    constexpr int kPer = 16 / sizeof(Elem), kTurn = 128 / sizeof(Elem);
+    __shared__ uint32_t box[kWaves][4][64];
+    const uint32_t b = p.first + blockIdx.x, tile = b / p.tiles_n;
+    if (tile >= tiles_of(p.experts, 16)) return;
+    const Span at = tile_rows(p.experts, 16, tile);
+    if (at.begin >= at.end) return;
+    const uint32_t o0 = b % p.tiles_n * 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t row = lane % 16, part = lane / 16;
+    const Elem* const a = static_cast<const Elem*>(p.a) + min(at.begin + row, at.end - 1) * p.a_stride;
+    const Elem* const w = static_cast<const Elem*>(p.w) + at.expert * p.w_expert + min(o0 + row, p.n - 1) * p.w_stride;
+    const int whole = (int)(p.k / kTurn);
+    Acc acc = {};
+    int turn = wave;
+    for (; turn + (kDeep - 1) * kWaves < whole; turn += kDeep * kWaves) {
+        u4 ga[kDeep][2], gw[kDeep][2];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t k = (turn + d * kWaves) * kTurn + (j * 4 + part) * kPer;
+                gw[d][j] = load16(w + k);
+                ga[d][j] = load16(a + k);
+            }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc = multiply_few<E>(gw[d][j], ga[d][j], acc);
+    }
+    for (; turn * kTurn < (int)p.k; turn += kWaves) {
+        u4 ga[2], gw[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t k = turn * kTurn + (j * 4 + part) * kPer;
+            gw[j] = turn < whole ? load16(w + k) : load16_cut(w, k, p.k);
+            ga[j] = turn < whole ? load16(a + k) : load16_cut(a, k, p.k);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc = multiply_few<E>(gw[j], ga[j], acc);
+    }
+    // register j of a lane: row 4*(lane/16) + j of w, row lane%16 of a
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const auto v = acc[j];
+        box[wave][j][lane] = __builtin_bit_cast(uint32_t, v);
+    }
+    __syncthreads();
+    const uint32_t c = threadIdx.x % 16, r = threadIdx.x / 16, t = at.begin + r, o = o0 + c;
+    if (t >= at.end || r >= 16 || o >= p.n) return;
+    typename std::conditional<std::is_same<E, I8>::value, int, float>::type sum = 0;
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) {
+        const uint32_t v = box[u][c % 4][c / 4 * 16 + r];
+        if constexpr (std::is_same<E, I8>::value)
+            sum += (int)v;
+        else
+            sum += from_bits(v);
+    }
+    float y;
+    if constexpr (std::is_same<E, I8>::value)
+        y = scaled(sum, p.a_scales[t], p.w_scales[(uint64_t)at.expert * p.n + o]);
+    else
+        y = sum;
+    typename Out::Elem* const out = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + o;
+    if (std::is_same<E, I8>::value && std::is_same<Out, F32>::value && p.accumulate) y += (float)*out;
+    *out = (typename Out::Elem)y;
+}
+
 // y from the slices' sums, added in order: eight columns of a row a thread.
 template <typename E, typename Out>
 __global__ __launch_bounds__(kThreads) void k_product_sum(ProductArgs p) {
@@ -528,6 +634,17 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool gro
     return best;
 }
 
+// Whether rows are so few that w's bytes alone count: 16 to an expert on
+// average, 32 in fp32, whose larger tile is slow.  Kernels for few rows and for
+// tiles (with slices), us with the launch, for 8 bits, bf16 and fp32:
+//   1 expert of 4096x4096, 16 rows    9, 12, 25 and 16, 19, 51
+//                          32 rows   12, 19, 38 and 17, 18, 51
+//                          64 rows   20, 33, 67 and 19, 19, 53
+//   16 of 2048x4096, 4 rows each     39, 60, 138 and 54, 82, 368
+//                    16 rows each    48, 83, 165 and 44, 82, 348
+//   32 of 1024x2048, 32 rows each    49, 74, 144 and 24, 41, 175
+bool few(uint64_t rows, uint64_t experts, int size) { return rows <= experts * (size == 4 ? 32 : 16); }
+
 uint64_t partial_row(uint64_t n) { return (n + 7) / 8 * 8; }
 uint64_t workspace_of(const Shape& s, uint64_t rows, uint64_t n) {
     return s.slices > 1 ? (s.slices * rows * partial_row(n) * 4 + 255) / 256 * 256 : 0;
@@ -542,6 +659,16 @@ int product(const char* name, ProductArgs p, void* workspace, size_t workspace_b
             const uint64_t blocks = ((uint64_t)p.experts.rows * p.n + kThreads - 1) / kThreads;
             return launch_blocks(name, st, blocks, kThreads, [&](uint64_t first, uint32_t here) {
                 k_product_narrow<E, kInner><<<here, kThreads, 0, st>>>(p, first);
+            });
+        }
+    }
+    if constexpr (!kInner) {
+        if (few(p.experts.rows, p.experts.count, sizeof(Elem))) {
+            p.tiles_n = (p.n + 15) / 16;
+            const uint64_t tiles_t = most_tiles(p.experts.rows, p.experts.count, 16, grouped);
+            return launch_blocks(name, st, tiles_t * p.tiles_n, 512, [&](uint64_t first, uint32_t blocks) {
+                p.first = (uint32_t)first;
+                k_product_few<E, Out><<<blocks, 512, 0, st>>>(p);
             });
         }
     }
@@ -583,8 +710,8 @@ bool valid_product(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts) {
 bool valid_offsets(const void* offsets, uint64_t experts) { return offsets ? aligned(offsets, 8) : experts == 1; }
 
 // Of one expert, with offsets and without: what either call may need.
-size_t product_workspace(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int size) {
-    if (rows < 1 || !valid_product(rows, n, k, experts)) return 0;
+size_t product_workspace(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int size, bool inner) {
+    if (rows < 1 || (!inner && few(rows, experts, size)) || !valid_product(rows, n, k, experts)) return 0;
     uint64_t bytes = workspace_of(shape_of(rows, n, k, experts, true, size), rows, n);
     if (experts == 1) bytes = std::max(bytes, workspace_of(shape_of(rows, n, k, 1, false, size), rows, n));
     return bytes;
@@ -620,19 +747,19 @@ extern "C" {
 
 size_t tlc_q8_product_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts) {
     const uint64_t stride = tlc_q8_code_stride(k);
-    return stride ? product_workspace(rows, n, stride, experts, 1) : 0;
+    return stride ? product_workspace(rows, n, stride, experts, 1, false) : 0;
 }
 
 size_t tlc_expert_product_workspace_size(uint64_t rows, uint64_t k, uint64_t n, uint64_t experts, int dtype) {
     if (!valid_dtype(dtype)) return 0;
     const int size = dtype == TLC_F32 ? 4 : 2;
-    return k < 16u / size ? 0 : product_workspace(rows, n, k, experts, size);
+    return k < 16u / size ? 0 : product_workspace(rows, n, k, experts, size, false);
 }
 
 size_t tlc_expert_input_grad_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, int dtype) {
     if (!valid_dtype(dtype)) return 0;
     const int size = dtype == TLC_F32 ? 4 : 2;
-    return std::min(n, k) < 16u / size ? 0 : product_workspace(rows, k, n, experts, size);
+    return std::min(n, k) < 16u / size ? 0 : product_workspace(rows, k, n, experts, size, true);
 }
 
 int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const int8_t* w, const float* w_scales,
