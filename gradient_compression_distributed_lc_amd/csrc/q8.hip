@@ -140,13 +140,14 @@ __global__ __launch_bounds__(kThreads) void k_column_max(ColumnArgs p) {
     const int n = (int)min((int64_t)p.cols - (int64_t)(c0 + unit * 8), (int64_t)8);
     const typename T::Elem* const x = static_cast<const typename T::Elem*>(p.x) + (uint64_t)(c0 + unit * 8);
     uint32_t m[8] = {};
-    for (uint32_t r = begin + r0; r < end; r += 32) {
-        Raw8<T> raw[4];
+    constexpr int kDeep = 8;  // rows under way
+    for (uint32_t r = begin + r0; r < end; r += 8 * kDeep) {
+        Raw8<T> raw[kDeep];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            raw[i] = load8<T>(x + (uint64_t)(r + i * 8) * p.x_stride, r + i * 8 < end ? n : 0);
+        for (int i = 0; i < kDeep; ++i)  // past the end the last row again
+            raw[i] = load8<T>(x + (uint64_t)min(r + i * 8, end - 1) * p.x_stride, n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kDeep; ++i) {
             float v[8];
             unpack8<T>(raw[i], v);
 #pragma unroll
@@ -169,29 +170,15 @@ __global__ __launch_bounds__(kThreads) void k_column_max(ColumnArgs p) {
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_pack_columns(ColumnArgs p) {
     __shared__ __align__(16) uint8_t box[128 * 128];
-    __shared__ float inverses[128];
+    __shared__ uint32_t most[2][128];
     const uint64_t b = p.first + blockIdx.x;
     const uint32_t band = (uint32_t)(b / p.blocks_c), c0 = (uint32_t)(b % p.blocks_c) * 128;
     const uint32_t tid = threadIdx.x;
-    if (tid < 128) {
-        uint32_t m = 0;
-        for (uint32_t k = 0; k < p.chunks; ++k) m = max(m, p.maxima[(uint64_t)k * p.padded + c0 + tid]);
-        float inverse;
-        const float scale = scale_for(m, &inverse);
-        inverses[tid] = inverse;
-        if (band == 0 && c0 + tid < p.cols) p.scales[c0 + tid] = scale;
-    }
-    __syncthreads();
     const uint32_t unit = tid % 16, quad = tid / 16;
     const int n = (int)min((int64_t)p.cols - (int64_t)(c0 + unit * 8), (int64_t)8);
-    float inverse[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) inverse[j] = inverses[unit * 8 + j];
     const typename T::Elem* const x = static_cast<const typename T::Elem*>(p.x) + (uint64_t)(c0 + unit * 8);
-    for (uint32_t t = 0; t < p.row_tiles; ++t) {
-        const uint32_t r0 = (band * p.row_tiles + t) * 128;
-        if (r0 >= p.code_row) break;
-        Raw8<T> raw[2][4];
+    Raw8<T> raw[2][4];
+    auto load = [&](uint32_t r0) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -199,6 +186,23 @@ __global__ __launch_bounds__(kThreads) void k_pack_columns(ColumnArgs p) {
                 const uint32_t r = r0 + h * 64 + quad * 4 + i;
                 raw[h][i] = load8<T>(x + (uint64_t)r * p.x_stride, r < p.rows ? n : 0);
             }
+    };
+    const uint32_t begin = band * p.row_tiles * 128, end = min(p.code_row, begin + p.row_tiles * 128);
+    load(begin);  // on its way while the maxima are joined
+    uint32_t m = 0;
+#pragma unroll 8
+    for (uint32_t k = tid / 128; k < p.chunks; k += 2)
+        m = max(m, p.maxima[(uint64_t)k * p.padded + c0 + tid % 128]);
+    most[tid / 128][tid % 128] = m;
+    __syncthreads();
+    float inverse[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = unit * 8 + j;
+        const float scale = scale_for(max(most[0][c], most[1][c]), &inverse[j]);
+        if (band == 0 && quad == 0 && c0 + c < p.cols) p.scales[c0 + c] = scale;
+    }
+    for (uint32_t r0 = begin; r0 < end; r0 += 128) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t q[4][8];
@@ -215,6 +219,7 @@ __global__ __launch_bounds__(kThreads) void k_pack_columns(ColumnArgs p) {
                 *reinterpret_cast<uint32_t*>(box + (unit * 8 + j) * 128 + (slot ^ (unit & 7)) * 16 + quad % 4 * 4) =
                     low_bytes(q[0][j], q[1][j], q[2][j], q[3][j]);
         }
+        if (r0 + 128 < end) load(r0 + 128);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
