@@ -47,36 +47,56 @@ struct ProductArgs {
     uint32_t first;                         // block of the whole that the launch begins with
 };
 
-// 32 rows by 32 rows over 32 bytes of the reduction: a lane holds 16 bytes of
-// row lane%32 on each side, the first or the second by lane/32.
-template <typename E>
+// A product of kRows rows by kRows rows, 32 over 32 bytes of the reduction or 16
+// over 64: a lane holds 16 bytes of row lane%kRows on either side, which ones by
+// lane/kRows.
+template <typename E, int kRows>
 struct Sums {
-    using Type = f16v;
+    using Type = typename std::conditional<kRows == 32, f16v, f4>::type;
 };
-template <>
-struct Sums<I8> {
-    using Type = i16v;
+template <int kRows>
+struct Sums<I8, kRows> {
+    using Type = typename std::conditional<kRows == 32, i16v, i4>::type;
 };
-template <typename E>
-__device__ __forceinline__ typename Sums<E>::Type multiply(u4 a, u4 b, typename Sums<E>::Type c) {
-    if constexpr (std::is_same<E, I8>::value)
-        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i4, a), __builtin_bit_cast(i4, b), c, 0, 0, 0);
-    else if constexpr (std::is_same<E, BF16>::value)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0,
-                                                       0);
-    else if constexpr (std::is_same<E, F16>::value)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0,
-                                                      0);
-    else {
+template <typename E, int kRows, typename Sum = typename Sums<E, kRows>::Type>
+__device__ __forceinline__ Sum multiply(u4 a, u4 b, Sum c) {
+    constexpr bool k32 = kRows == 32;
+    if constexpr (std::is_same<E, I8>::value) {
+        const i4 x = __builtin_bit_cast(i4, a), y = __builtin_bit_cast(i4, b);
+        if constexpr (k32)
+            return __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+    } else if constexpr (std::is_same<E, BF16>::value) {
+        const b8v x = __builtin_bit_cast(b8v, a), y = __builtin_bit_cast(b8v, b);
+        if constexpr (k32)
+            return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+    } else if constexpr (std::is_same<E, F16>::value) {
+        const h8v x = __builtin_bit_cast(h8v, a), y = __builtin_bit_cast(h8v, b);
+        if constexpr (k32)
+            return __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, c, 0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)  // the reduction's order inside the 8 does not matter where both sides have it
-            c = __builtin_amdgcn_mfma_f32_32x32x2f32(from_bits(a[j]), from_bits(b[j]), c, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {  // the reduction's order inside does not matter where both sides have it
+            if constexpr (k32)
+                c = __builtin_amdgcn_mfma_f32_32x32x2f32(from_bits(a[j]), from_bits(b[j]), c, 0, 0, 0);
+            else
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(from_bits(a[j]), from_bits(b[j]), c, 0, 0, 0);
+        }
         return c;
     }
 }
 
+// `bytes` behind a pointer that all lanes share.  The compiler is kept from
+// taking the sum apart, or a loop's loads would have a 64-bit pointer in
+// registers each instead of one and 32-bit distances.
 template <typename Elem>
 __device__ __forceinline__ const Elem* later(const Elem* p, uint32_t bytes) {
+    asm("" : "+v"(bytes));
     return reinterpret_cast<const Elem*>(reinterpret_cast<const char*>(p) + bytes);
 }
 
@@ -124,24 +144,32 @@ __device__ __forceinline__ s4v read_tr(const void* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)p);
 }
 
-// The order of instructions among kProducts products, each of which keeps the
-// matrix core busy for 32 clocks: LDS reads, LDS writes and loads, each kind
-// spread evenly over them.
+// The order of instructions among kProducts products: LDS reads, LDS writes and
+// loads, each kind spread evenly over them, and the kinds apart from each other.
 template <int kProducts, int kReads, int kWrites, int kLoads>
 __device__ __forceinline__ void interleave() {
+    // how many of n have come by the i-th product, each `early` quarters of its distance before the even place
+    constexpr auto by = [](int i, int n, int early) { return n ? (4 * i * n + early * kProducts) / (4 * kProducts) : 0; };
 #pragma unroll
     for (int i = 0; i < kProducts; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
 #pragma unroll
-        for (int r = i * kReads / kProducts; r < (i + 1) * kReads / kProducts; ++r)
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        for (int r = by(i, kReads, 0); r < by(i + 1, kReads, 0); ++r) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
 #pragma unroll
-        for (int r = i * kWrites / kProducts; r < (i + 1) * kWrites / kProducts; ++r)
+        for (int r = by(i, kWrites, 3); r < by(i + 1, kWrites, 3); ++r)
             __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
 #pragma unroll
-        for (int r = i * kLoads / kProducts; r < (i + 1) * kLoads / kProducts; ++r)
+        for (int r = by(i, kLoads, 1); r < by(i + 1, kLoads, 1); ++r)
             __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
+}
+
+// Inner weights of 16 bits: the 16-byte slots (8 columns) of row r lie at
+// slot ^ swizzle(r), so that what half a wavefront reads at once, 4 rows of 32
+// columns or 8 rows of 16, falls into the 64 banks once each.
+template <int kRows>
+__device__ __forceinline__ int swizzle(int r) {
+    return (r & 3) << 2 | (r & 1) | (kRows == 16 ? (r >> 3 & 1) << 1 : 0);
 }
 
 // A block computes kTile x kTile values of y, each of its four wavefronts a
@@ -150,16 +178,18 @@ __device__ __forceinline__ void interleave() {
 // Two stages of LDS.  While one is multiplied, the step loaded before goes to
 // the other, and as its registers are freed the step after is loaded into them:
 // a load has a whole step's products to arrive in.  The block meets once a step,
-// before the last quarter of the products, whose operands it has then read;
-// these run while the next stage's first operands are read.
+// before the last part of the products, whose operands it has then read; these
+// run while the next stage's first operands are read.
 template <typename E, typename Out, bool kInner, int kTile>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(ProductArgs p) {
     using Elem = typename E::Elem;
-    using Acc = typename Sums<E>::Type;
+    constexpr int kRows = sizeof(Elem) == 4 || (kInner && kTile == 256) ? 32 : 16;  // of a product
+    constexpr int kParts = 64 / kRows, kSubs = 8 / kParts;     // 16-byte chunks of a row in it; of them in a step
+    using Acc = typename Sums<E, kRows>::Type;
     constexpr int kPer = 16 / sizeof(Elem);       // elements of a 16-byte chunk
     constexpr int kStep = 128 / sizeof(Elem);     // of the reduction in a step
     constexpr int kLoads = kTile * 8 / kThreads;  // chunks a lane, of either operand
-    constexpr int kWave = kTile / 2, kTiles = kWave / 32;
+    constexpr int kWave = kTile / 2, kTiles = kWave / kRows;
     struct Stage {
         u4 a[kTile * 8], w[kTile * 8];
     };
@@ -200,9 +230,11 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     static_assert(kInnerRows % 4 == 0, "a lane's rows have one swizzle");
     const int inner_row = tid / kChunks;
     const int inner_chunk = tid % kChunks;
-    const int place_w = !kInner              ? place_a
-                        : sizeof(Elem) == 2 ? inner_row * kChunks + (inner_chunk ^ ((inner_row & 3) << 2 | (inner_row & 1)))
-                                            : tid;
+    auto place_w = [&](int i) {
+        if constexpr (!kInner) return i * kThreads + place_a;
+        const int r = inner_row + i * kInnerRows;
+        return r * kChunks + (sizeof(Elem) == 2 ? inner_chunk ^ swizzle<kRows>(r) : inner_chunk);
+    };
     const uint32_t inner_col = o0 + inner_chunk * kPer;
 
     uint32_t from_a[kLoads], from_w[kInner ? 1 : kLoads];  // bytes
@@ -218,8 +250,6 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
             from_w[i] = min((uint32_t)row + i * 32, last_w) * (uint32_t)(p.w_stride * sizeof(Elem)) + chunk * 16;
     }
     u4 ga[kLoads], gw[kLoads];
-    // The first or the last chunks of a whole step.
-    constexpr int kEarly = kLoads * 3 / 4;
     auto load_whole = [&](int s, int from, int to) {
         const Elem* const pa = a + (uint64_t)s * kStep;
         const Elem* const pw = w + (uint64_t)s * kStep * (kInner ? p.w_stride : 1);
@@ -230,12 +260,12 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
                                   : later(pw, from_w[kInner ? 0 : i]));
         }
     };
-    auto load = [&](int s) {
-        if (s < whole) return load_whole(s, 0, kLoads);
+    auto load = [&](int s, int from, int to) {
+        if (s < whole) return load_whole(s, from, to);
         // in the whole row, which has sixteen bytes where a slice's end may not
         const uint32_t k0 = k_first + s * kStep + chunk * kPer;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
+        for (int i = from; i < to; ++i) {
             ga[i] = load16_cut(later(a - k_first, from_a[i] - chunk * 16), k0, p.k);
             if constexpr (!kInner) {
                 gw[i] = load16_cut(later(w - k_first, from_w[i] - chunk * 16), k0, p.k);
@@ -246,34 +276,33 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
             }
         }
     };
-    auto store = [&](Stage& st) {
+    auto store = [&](Stage& st, int from, int to) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
+        for (int i = from; i < to; ++i) {
             st.a[i * kThreads + place_a] = ga[i];
-            st.w[i * kThreads + place_w] = gw[i];
+            st.w[place_w(i)] = gw[i];
         }
     };
 
     const int wi = (wave >> 1) * kWave, wc = (wave & 1) * kWave;
-    const int r32 = lane & 31, half = lane >> 5;
+    const int r_lane = lane % kRows, part = lane / kRows;
     Acc acc[kTiles][kTiles] = {};
-    auto operand_rows = [&](const u4* st, int sub, int from) {  // of 32 rows beginning with `from`
-        return st[(from + r32) * 8 + ((sub * 2 + half) ^ (r32 >> 1 & 7))];
+    auto operand_rows = [&](const u4* st, int sub, int from) {  // of kRows rows beginning with `from`
+        return st[(from + r_lane) * 8 + ((sub * kParts + part) ^ (r_lane >> 1 & 7))];
     };
     // Columns of rows of the reduction.  16 bits: the transposing read gives
-    // each of 16 lanes 4 rows of one column from 4 rows of 16 columns; the
-    // 16-byte slots (8 columns) of row r lie at slot ^ (r%4*4 | r%2), so that
-    // the 4 rows x 32 columns read at once fall into the 64 banks once each.
+    // each of 16 lanes 4 rows of one column from 4 rows of 16 columns.
     auto operand_columns = [&](const u4* st, int sub, int from) {
         if constexpr (sizeof(Elem) == 2) {
-            const int r = half * 8 + (lane >> 2 & 3);
-            const int slot = from / 8 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1);
-            const char* q = reinterpret_cast<const char*>(st) + (sub * 16 + r) * kTile * 2 +
-                            (slot ^ ((r & 3) << 2 | (r & 1))) * 16 + (lane & 1) * 8;
+            const int r = part * 8 + (lane >> 2 & 3);
+            const int slot = from / 8 + (kRows == 32 ? (lane >> 4 & 1) * 2 : 0) + (lane >> 1 & 1);
+            const char* q = reinterpret_cast<const char*>(st) + (sub * kParts * 8 + r) * kTile * 2 +
+                            (slot ^ swizzle<kRows>(r)) * 16 + (lane & 1) * 8;
             const s4v lo = read_tr(q), hi = read_tr(q + 4 * kTile * 2);
             return __builtin_bit_cast(u4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(st) + (sub * 8 + half * 4) * kTile + from + r32;
+            const uint32_t* q =
+                reinterpret_cast<const uint32_t*>(st) + (sub * kParts * 4 + part * 4) * kTile + from + r_lane;
             return u4{q[0], q[kTile], q[2 * kTile], q[3 * kTile]};
         }
     };
@@ -281,52 +310,58 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     auto operands = [&](const Stage& st, int sub) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
-            fw[sub & 1][i] = kInner ? operand_columns(st.w, sub, wc + i * 32) : operand_rows(st.w, sub, wc + i * 32);
+            fw[sub & 1][i] =
+                kInner ? operand_columns(st.w, sub, wc + i * kRows) : operand_rows(st.w, sub, wc + i * kRows);
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) fa[sub & 1][i] = operand_rows(st.a, sub, wi + i * 32);
+        for (int i = 0; i < kTiles; ++i) fa[sub & 1][i] = operand_rows(st.a, sub, wi + i * kRows);
     };
     auto products = [&](const u4* ra, const u4* rw) {
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E>(ra[i], rw[c], acc[i][c]);
+            for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E, kRows>(ra[i], rw[c], acc[i][c]);
     };
     constexpr bool kSchedule = sizeof(Elem) <= 2;
-    constexpr int kProducts = kTiles * kTiles, kReads = kTiles * (kInner ? 3 : 2);  // of a quarter, 16 bits or 8
-    // Step s multiplies `now`, stores step s + 1 to `next` and loads step s + 2.
-    // kMain: all of it, of whole steps, without a branch, so that one schedule
-    // spans it.
+    constexpr int kProducts = kTiles * kTiles, kReads = kTiles * (kInner ? 3 : 2);  // of a sub-step, 16 bits or 8
+    // Step s multiplies `now`.  Half of the chunks of step s + 1 are in `next`
+    // when it begins; it stores the others and, when `now` has been read, the
+    // first half of step s + 2, and loads into each register that frees what will
+    // be stored from it a step later.  kMain: all of it, of whole steps, without
+    // a branch, so that one schedule spans it.
+    constexpr int kFirst = kLoads * (kSubs == 2 ? 2 : 1) / 4;  // chunks of the first part, by its share of the products
     auto step = [&](Stage& now, Stage& next, int s, auto main) {
         constexpr bool kMain = decltype(main)::value;
-        if (!kMain && s + 1 >= 0 && s + 1 < steps) store(next);
-        if (!kMain && s + 2 < steps) load(s + 2);
+        if (kMain || (s + 1 >= 0 && s + 1 < steps)) store(next, kFirst, kLoads);
+        if constexpr (kMain)
+            load_whole(s + 2, kFirst, kLoads);
+        else if (s + 2 >= 0 && s + 2 < steps)
+            load(s + 2, kFirst, kLoads);
         if (kMain || s >= 0) {
 #pragma unroll
-            for (int sub = 0; sub < 3; ++sub) {
+            for (int sub = 0; sub < kSubs - 1; ++sub) {
                 operands(now, sub + 1);
                 products(fa[sub & 1], fw[sub & 1]);
             }
         }
-        if constexpr (kMain) {
-            store(next);
-            load_whole(s + 2, 0, kEarly);
-            if constexpr (kSchedule) interleave<3 * kProducts, 3 * kReads, 2 * kLoads, 2 * kEarly>();
-        }
+        if constexpr (kMain && kSchedule)
+            interleave<(kSubs - 1) * kProducts, (kSubs - 1) * kReads, 2 * (kLoads - kFirst), 2 * (kLoads - kFirst)>();
         __syncthreads();
         u4 la[kTiles], lw[kTiles];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) la[i] = fa[1][i], lw[i] = fw[1][i];
         if (kMain || (s + 1 >= 0 && s + 1 < steps)) operands(next, 0);
+        if (kMain || (s + 2 >= 0 && s + 2 < steps)) store(now, 0, kFirst);
+        if constexpr (kMain)
+            load_whole(s + 3, 0, kFirst);
+        else if (s + 3 < steps)
+            load(s + 3, 0, kFirst);
         if (kMain || s >= 0) products(la, lw);
-        if constexpr (kMain) {
-            load_whole(s + 2, kEarly, kLoads);
-            if constexpr (kSchedule) interleave<kProducts, kReads, 0, 2 * (kLoads - kEarly)>();
-        }
+        if constexpr (kMain && kSchedule) interleave<kProducts, kReads, 2 * kFirst, 2 * kFirst>();
     };
     // The steps before 0 fill the pipeline.
-    for (int s = -2; s < steps; ++s) {
+    for (int s = -3; s < steps; ++s) {
         if (s >= 0 && s % 2 == 0)
-            for (; s + 3 < whole; s += 2) {
+            for (; s + 4 < whole; s += 2) {
                 step(stage0, stage1, s, Int<1>{});
                 step(stage1, stage0, s + 1, Int<1>{});
             }
@@ -334,7 +369,8 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     }
     __syncthreads();
 
-    // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32.
+    // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32 (of
+    // 16 rows: row 4*(lane/16) + j, column lane%16).
     // 64 rows at a time through LDS, so that a lane has eight values of a row.
     // Short loops: code that runs once costs more to fetch than to run.
     static_assert(2 * sizeof(Stage) >= 4 * 64 * kWave * sizeof(uint32_t), "the wavefronts' rows fit");
@@ -349,16 +385,19 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
         for (int j = 0; j < 8; ++j) sw[j] = j < count ? p.w_scales[(uint64_t)at.expert * p.n + col + j] : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kTiles; i += 2) {
+    for (int i = 0; i < kTiles; i += 64 / kRows) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int h = 0; h < 64 / kRows; ++h)
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-                const auto v = acc[i + j / 16][c][j % 16];
-                mine[(j / 4 * 8 + half * 4 + j % 4) * kWave + c * 32 + r32] = __builtin_bit_cast(uint32_t, v);
-            }
+            for (int j = 0; j < kRows * kRows / 64; ++j)
+#pragma unroll
+                for (int c = 0; c < kTiles; ++c) {
+                    const auto v = acc[i + h][c][j];
+                    const int r = h * kRows + (kRows == 32 ? j / 4 * 8 + part * 4 + j % 4 : part * 4 + j);
+                    mine[r * kWave + c * kRows + r_lane] = __builtin_bit_cast(uint32_t, v);
+                }
         wave_sync();
-        const uint32_t t0 = at.begin + wi + i * 32;
+        const uint32_t t0 = at.begin + wi + i * kRows;
 #pragma unroll 1
         for (int q = 0; q < 64 && t0 + q < at.end; q += kDown * kDeep) {
             u4 in[kDeep][2];
@@ -426,37 +465,11 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 // wavefronts and 8 turns under way measured the same or slower (1x8192x4096
 // bf16 17.0 us with its launch; 16.8 to 28.3).  A row of 8192x4096 bf16, 67 MB,
 // takes about 11 us of its own, 16 rows of 8192x8192 40.
-template <typename E>
-struct FewSums {
-    using Type = f4;
-};
-template <>
-struct FewSums<I8> {
-    using Type = i4;
-};
-template <typename E>
-__device__ __forceinline__ typename FewSums<E>::Type multiply_few(u4 a, u4 b, typename FewSums<E>::Type c) {
-    if constexpr (std::is_same<E, I8>::value)
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, a), __builtin_bit_cast(i4, b), c, 0, 0, 0);
-    else if constexpr (std::is_same<E, BF16>::value)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8v, a), __builtin_bit_cast(b8v, b), c, 0, 0,
-                                                       0);
-    else if constexpr (std::is_same<E, F16>::value)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, a), __builtin_bit_cast(h8v, b), c, 0, 0,
-                                                      0);
-    else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(from_bits(a[j]), from_bits(b[j]), c, 0, 0, 0);
-        return c;
-    }
-}
-
 template <typename E, typename Out>
 __global__ __launch_bounds__(512) void k_product_few(ProductArgs p) {
     constexpr int kWaves = 8, kDeep = 4;  // turns under way
     using Elem = typename E::Elem;
-    using Acc = typename FewSums<E>::Type;
+    using Acc = typename Sums<E, 16>::Type;
     constexpr int kPer = 16 / sizeof(Elem), kTurn = 128 / sizeof(Elem);
     __shared__ uint32_t box[kWaves][4][64];
     const uint32_t b = p.first + blockIdx.x, tile = b / p.tiles_n;
@@ -484,7 +497,7 @@ __global__ __launch_bounds__(512) void k_product_few(ProductArgs p) {
 #pragma unroll
         for (int d = 0; d < kDeep; ++d)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc = multiply_few<E>(gw[d][j], ga[d][j], acc);
+            for (int j = 0; j < 2; ++j) acc = multiply<E, 16>(gw[d][j], ga[d][j], acc);
     }
     for (; turn * kTurn < (int)p.k; turn += kWaves) {
         u4 ga[2], gw[2];
@@ -495,7 +508,7 @@ __global__ __launch_bounds__(512) void k_product_few(ProductArgs p) {
             ga[j] = turn < whole ? load16(a + k) : load16_cut(a, k, p.k);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc = multiply_few<E>(gw[j], ga[j], acc);
+        for (int j = 0; j < 2; ++j) acc = multiply<E, 16>(gw[j], ga[j], acc);
     }
     // register j of a lane: row 4*(lane/16) + j of w, row lane%16 of a
 #pragma unroll
