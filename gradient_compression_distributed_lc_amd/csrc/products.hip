@@ -321,14 +321,15 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll
             for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E, kRows>(ra[i], rw[c], acc[i][c]);
     };
-    constexpr bool kSchedule = sizeof(Elem) <= 2;
-    constexpr int kProducts = kTiles * kTiles, kReads = kTiles * (kInner ? 3 : 2);  // of a sub-step, 16 bits or 8
-    // Step s multiplies `now`.  Half of the chunks of step s + 1 are in `next`
-    // when it begins; it stores the others and, when `now` has been read, the
-    // first half of step s + 2, and loads into each register that frees what will
-    // be stored from it a step later.  kMain: all of it, of whole steps, without
-    // a branch, so that one schedule spans it.
-    constexpr int kFirst = kLoads * (kSubs == 2 ? 2 : 1) / 4;  // chunks of the first part, by its share of the products
+    // of a sub-step; the inner fp32 weight is read value by value and left to the compiler
+    constexpr bool kSchedule = sizeof(Elem) <= 2 || !kInner;
+    constexpr int kProducts = kTiles * kTiles * (sizeof(Elem) == 4 ? 4 : 1), kReads = kTiles * (kInner ? 3 : 2);
+    // Step s multiplies `now`.  The first chunks of step s + 1 are in `next` when
+    // it begins; it stores the others and, when `now` has been read, the first
+    // ones of step s + 2, and loads into each register that frees what will be
+    // stored from it a step later.  kMain: all of it, of whole steps, without a
+    // branch, so that one schedule spans it.
+    constexpr int kFirst = kLoads / kSubs;  // those stored during the last sub-step
     auto step = [&](Stage& now, Stage& next, int s, auto main) {
         constexpr bool kMain = decltype(main)::value;
         if (kMain || (s + 1 >= 0 && s + 1 < steps)) store(next, kFirst, kLoads);
