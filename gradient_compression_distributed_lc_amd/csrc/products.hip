@@ -648,16 +648,18 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool gro
     return best;
 }
 
-// Whether rows are so few that w's bytes alone count: 16 to an expert on
-// average, 32 in fp32, whose larger tile is slow.  Kernels for few rows and for
-// tiles (with slices), us with the launch, for 8 bits, bf16 and fp32:
+// Whether rows are so few that w's bytes alone count: 8 to an expert on average
+// and 16 more, in fp32, whose larger tile is slow, 32 to an expert.  Rows may all
+// be one expert's, whose weight is then read once for each 16 of them, so no
+// more than where both measured the same.  Kernels for few rows and for tiles
+// (with slices), us with the launch, in 8 bits, bf16 and fp32:
 //   1 expert of 4096x4096, 16 rows    9, 12, 25 and 16, 19, 51
 //                          32 rows   12, 19, 38 and 17, 18, 51
 //                          64 rows   20, 33, 67 and 19, 19, 53
 //   16 of 2048x4096, 4 rows each     39, 60, 138 and 54, 82, 368
 //                    16 rows each    48, 83, 165 and 44, 82, 348
 //   32 of 1024x2048, 32 rows each    49, 74, 144 and 24, 41, 175
-bool few(uint64_t rows, uint64_t experts, int size) { return rows <= experts * (size == 4 ? 32 : 16); }
+bool few(uint64_t rows, uint64_t experts, int size) { return rows <= (size == 4 ? 32 * experts : 8 * experts + 16); }
 
 uint64_t partial_row(uint64_t n) { return (n + 7) / 8 * 8; }
 uint64_t workspace_of(const Shape& s, uint64_t rows, uint64_t n) {

@@ -126,6 +126,18 @@ def test_pack_special_values(tlc, cols):
         assert torch.equal(torch.nan_to_num(got.scales.cpu(), nan=-1.0), torch.nan_to_num(scales, nan=-1.0))
 
 
+def test_pack_rows_of_more_than_one_launch(tlc):
+    """2^26 rows of 64 lanes are 2^32 threads, which HIP takes in two launches."""
+    rows = 2 ** 26 + 5
+    x = torch.zeros(rows, 1, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 2 ** 25, 2 ** 26 - 8, 2 ** 26 - 4, 2 ** 26, 2 ** 26 + 4], device="cuda")
+    x[at, 0] = torch.arange(1, 8, device="cuda").bfloat16()
+    q = tlc.q8_pack_rows(x)
+    assert (q.codes[at, 0] == 127).all() and not q.codes[at, 1:].any()
+    assert torch.equal(q.scales[at].cpu(), torch.arange(1, 8).float() / torch.full((7,), 127.0))
+    assert int((q.codes[:, 0] != 0).sum()) == 7
+
+
 # ---- the product of 8-bit integers -------------------------------------------
 
 
@@ -196,6 +208,9 @@ def test_product8_scales_that_meet_at_the_ends_of_the_range(tlc):
     assert torch.equal(y[fits].double(), want[fits])  # scales are powers of two, sums below 2^24
     assert torch.isnan(y[:, 4]).all()
     assert torch.isinf(y[1, 0]) and torch.isinf(y[1, 2])
+    sa[2] = math.nan
+    y = tlc.q8_product(rows8(tlc, a, sa, k), rows8(tlc, w, sw, k), torch.float32).cpu()
+    assert torch.isnan(y[2]).all() and not torch.isnan(y[3, :4]).any()
 
 
 @pytest.mark.parametrize("rows,n,k", [(5, 40, 64), (200, 300, 515)])
@@ -304,10 +319,32 @@ def test_expert_products(tlc, rows, k, n, experts, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [3, 200])
+def test_values_below_the_normal_range(tlc, rows, dtype):
+    """Subnormal inputs count with their value, and subnormal results are rounded to their step."""
+    k, n = 96, 40
+    g = gen(11)
+    least = {torch.float32: -149, torch.float16: -24, torch.bfloat16: -133}[dtype]
+    x = whole(g, rows, k, most=3).double() * 2.0 ** least
+    x, up = x.to(dtype), 2.0 ** (20 if dtype != torch.float16 else 10)
+    assert (x != 0).any()
+    for factor in (up, 0.25):
+        w = (whole(g, 1, n, k, most=3).double() * factor).to(dtype)
+        # In 16 bits fp32 holds every product and sum exactly.  In fp32 a quarter of the least step is no fp32 number:
+        # each of the k additions rounds to a multiple of 2^-149, by 2^-150 at most.
+        inside = k * 2.0 ** -150 if dtype == torch.float32 and factor < 1 else 0.0
+        want = (x.double() @ w[0].double().t()).to(dtype).double()
+        bound = torch.full_like(want, inside + (2.0 ** -150 if inside else 0.0))  # and the reference's own rounding
+        assert_close(tlc.expert_product(x.cuda(), w.cuda()), want, bound, ("y", factor))
+        back = w.transpose(1, 2).contiguous().cuda()
+        assert_close(tlc.expert_input_grad(x.cuda(), back), want, bound, ("dx", factor))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("k", [1027, 2050, 4099, 8191])
-def test_long_reductions_of_few_rows(tlc, k, dtype):
+def test_long_reductions(tlc, k, dtype):
     """Few tiles and a long reduction, whose slices end at odd places: the last one may be shorter than 16 bytes."""
-    rows, n, counts = 40, 72, [25, 0, 15]
+    rows, n, counts = 140, 72, [85, 0, 55]
     g = gen(k)
     x, w = whole(g, rows, k, dtype=dtype, most=1), whole(g, 3, n, k, dtype=dtype, most=1)
     off = offsets_of(counts).cuda()
@@ -321,6 +358,45 @@ def test_long_reductions_of_few_rows(tlc, k, dtype):
     y8 = tlc.q8_product(*[rows8(tlc, c, torch.ones(c.shape[0]), k) for c, _ in q], torch.float32, offsets=off)
     for e, (b, t) in enumerate(ref.spans(off.tolist(), rows)):
         assert torch.equal(y8[b:t].cpu(), (q[0][0][b:t].double() @ q[1][0][e * n:(e + 1) * n].double().t()).float())
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("k", [1096, 1027])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_large_ragged_products_of_whole_numbers_are_exact(tlc, dtype, k, pad):
+    """Sizes that take the larger tile (in 16 bits and 8), with a ragged last one in every direction."""
+    counts, n, before, behind = [1700, 1900], 4091, 3, 5
+    say(f"large products {dtype} k={k} pad={pad}")
+    g = gen(k + pad)
+    offsets, rows = offsets_of(counts, before), before + sum(counts) + behind
+    off = offsets.cuda()
+    x, w = whole(g, rows, k, dtype=dtype), whole(g, 2, n, k, dtype=dtype)
+    back = w.transpose(1, 2).contiguous()
+    y = strided(torch.full((rows, n), math.nan, dtype=dtype), pad)
+    z = strided(torch.full((rows, n), math.nan, dtype=dtype), pad)
+    tlc.expert_product(strided(x, pad), strided(w, pad), off, y=y)
+    tlc.expert_input_grad(strided(x, pad), strided(back, pad), off, dx=z)
+    for v in (y, z):
+        assert torch.isnan(v[:before]).all() and torch.isnan(v[rows - behind:]).all()
+        for e, (b, t) in enumerate(ref.spans(offsets.tolist(), rows)):
+            want = (x[b:t].cuda().float() @ w[e].cuda().float().t()).to(dtype)  # whole numbers below 2^24
+            assert torch.equal(v[b:t], want), e
+
+
+def test_large_ragged_product8_is_exact(tlc):
+    counts, n, k = [1700, 1900], 4091, 2055
+    g = gen(21)
+    off = offsets_of(counts).cuda()
+    a, w = [torch.randint(-80, 81, (r, k), generator=g).to(torch.int8) for r in (3600, 2 * n)]
+    pads = torch.nn.functional.pad
+    q = [tlc.Rows8(pads(c, (0, 2176 - k)).cuda(), torch.ones(c.shape[0], device="cuda"), k) for c in (a, w)]
+    y = tlc.q8_product(*q, torch.float32, offsets=off)
+    z = torch.zeros_like(y)
+    tlc.q8_product(*q, torch.float32, offsets=off, y=z, accumulate=True)
+    assert torch.equal(y, z)
+    for e, (b, t) in enumerate(ref.spans(off.tolist(), 3600)):
+        want = a[b:t].cuda().float() @ w[e * n:(e + 1) * n].cuda().float().t()  # 2055 * 80 * 80 is below 2^24
+        assert torch.equal(y[b:t], want), e
 
 
 def test_offsets_that_are_not_in_order(tlc):
