@@ -361,11 +361,16 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     };
     // The steps before 0 fill the pipeline.
     for (int s = -3; s < steps; ++s) {
-        if (s >= 0 && s % 2 == 0)
+        if (s >= 0 && s % 2 == 0 && s + 4 < whole) {
+            // Nothing under way at the loop's beginning: else the compiler, which
+            // does not know how much that is, waits in every turn for loads that
+            // were only just sent off (vmcnt(7) in place of 15).
+            __builtin_amdgcn_s_waitcnt(0x0F70);
             for (; s + 4 < whole; s += 2) {
                 step(stage0, stage1, s, Int<1>{});
                 step(stage1, stage0, s + 1, Int<1>{});
             }
+        }
         step(s & 1 ? stage1 : stage0, s & 1 ? stage0 : stage1, s, Int<0>{});
     }
     __syncthreads();
