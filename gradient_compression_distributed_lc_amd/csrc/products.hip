@@ -319,7 +319,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E, kRows>(ra[i], rw[c], acc[i][c]);
+            for (int c = 0; c < kTiles; ++c) acc[i][c] = multiply<E, kRows>(rw[c], ra[i], acc[i][c]);
     };
     // of a sub-step; the inner fp32 weight is read value by value and left to the compiler
     constexpr bool kSchedule = sizeof(Elem) <= 2 || !kInner;
@@ -375,12 +375,13 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     }
     __syncthreads();
 
-    // register j of a lane: row 8*(j/4) + 4*(lane/32) + j%4, column lane%32 (of
-    // 16 rows: row 4*(lane/16) + j, column lane%16).
-    // 64 rows at a time through LDS, so that a lane has eight values of a row.
+    // register j of a lane: row lane%16, column 4*(lane/16) + j (of 32 rows: row
+    // lane%32, column 8*(j/4) + 4*(lane/32) + j%4).
+    // 64 rows at a time through LDS, so that a lane has eight values of a row: 16
+    // bytes of row r at place ^ (r%16), which spreads a column over the banks.
     // Short loops: code that runs once costs more to fetch than to run.
     static_assert(2 * sizeof(Stage) >= 4 * 64 * kWave * sizeof(uint32_t), "the wavefronts' rows fit");
-    uint32_t* const mine = reinterpret_cast<uint32_t*>(wave < 2 ? &stage0 : &stage1) + wave % 2 * 64 * kWave;
+    u4* const mine = reinterpret_cast<u4*>(wave < 2 ? &stage0 : &stage1) + wave % 2 * 16 * kWave;
     constexpr int kAcross = kWave / 8, kDown = 64 / kAcross, kDeep = 4;
     const uint32_t col = o0 + wc + lane % kAcross * 8;
     const int count = (int)min((int64_t)p.n - (int64_t)col, (int64_t)8);
@@ -395,12 +396,13 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll
         for (int h = 0; h < 64 / kRows; ++h)
 #pragma unroll
-            for (int j = 0; j < kRows * kRows / 64; ++j)
+            for (int c = 0; c < kTiles; ++c)
 #pragma unroll
-                for (int c = 0; c < kTiles; ++c) {
-                    const auto v = acc[i + h][c][j];
-                    const int r = h * kRows + (kRows == 32 ? j / 4 * 8 + part * 4 + j % 4 : part * 4 + j);
-                    mine[r * kWave + c * kRows + r_lane] = __builtin_bit_cast(uint32_t, v);
+                for (int j = 0; j < kRows * kRows / 64; j += 4) {
+                    const auto& v = acc[i + h][c];
+                    const int r = h * kRows + r_lane, to = (c * kRows + j * 2) / 4 + part;
+                    *reinterpret_cast<typename Sums<E, 16>::Type*>(mine + r * (kWave / 4) + (to ^ (r & 15))) =
+                        typename Sums<E, 16>::Type{v[j], v[j + 1], v[j + 2], v[j + 3]};
                 }
         wave_sync();
         const uint32_t t0 = at.begin + wi + i * kRows;
@@ -411,8 +413,8 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll
             for (int d = 0; d < kDeep; ++d) {
                 const uint32_t r = q + d * kDown + lane / kAcross;
-                const u4* const from = reinterpret_cast<const u4*>(mine + r * kWave + lane % kAcross * 8);
-                in[d][0] = from[0], in[d][1] = from[1];
+                const u4* const from = mine + r * (kWave / 4);
+                in[d][0] = from[lane % kAcross * 2 ^ (r & 15)], in[d][1] = from[(lane % kAcross * 2 + 1) ^ (r & 15)];
                 if constexpr (std::is_same<E, I8>::value) sa[d] = p.a_scales[min(t0 + r, at.end - 1)];
             }
 #pragma unroll
@@ -450,7 +452,9 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll 1
             for (uint32_t c = ragged; c < p.n; ++c) {
                 typename Out::Elem* const o = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + c;
-                const uint32_t u = mine[lane * kWave + c - (o0 + wc)];
+                const uint32_t in_row = c - (o0 + wc);
+                const uint32_t u = reinterpret_cast<const uint32_t*>(
+                    mine + lane * (kWave / 4) + (in_row / 4 ^ (lane & 15)))[in_row % 4];
                 float v;
                 if constexpr (std::is_same<E, I8>::value)
                     v = scaled((int)u, p.a_scales[t], p.w_scales[(uint64_t)at.expert * p.n + c]);
