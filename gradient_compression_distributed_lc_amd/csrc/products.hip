@@ -127,11 +127,13 @@ __device__ __forceinline__ u4 load16_cut(const Elem* row, uint32_t first, uint32
     return u4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-// The scales' product with a sum: the smaller scale first, so that nothing
-// leaves fp32's range on the way that the result does not.  Three roundings.
+// A sum times the scales, a's first: a scale is at least 2^-126 and a sum that
+// is not 0 at least 1, so that nothing is lost below; where a's scale is so large
+// that this could leave fp32's range above, w's first.  Three roundings.
+constexpr float kFar = 0x1p96f;
 __device__ __forceinline__ float scaled(int sum, float sa, float sw) {
-    const bool below = sa < sw;  // false with a NaN, which then stays in one of the two
-    return (float)sum * (below ? sa : sw) * (below ? sw : sa);
+    const bool far = sa > kFar;
+    return (float)sum * (far ? sw : sa) * (far ? sa : sw);
 }
 
 // Orders a wavefront's own LDS accesses across its lanes.
@@ -391,8 +393,17 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
 #pragma unroll
         for (int j = 0; j < 8; ++j) sw[j] = j < count ? p.w_scales[(uint64_t)at.expert * p.n + col + j] : 0.0f;
     }
+    float row_scales[kTiles * kRows / 64] = {};  // a row a lane
+    if constexpr (std::is_same<E, I8>::value) {
+#pragma unroll
+        for (int g = 0; g < kTiles * kRows / 64; ++g)
+            row_scales[g] = p.a_scales[min(at.begin + wi + g * 64 + lane, at.end - 1)];
+    }
 #pragma unroll
     for (int i = 0; i < kTiles; i += 64 / kRows) {
+        // a's scales that large are rare: the usual order alone saves two of six operations a value
+        const float mine_sa = row_scales[i * kRows / 64];
+        const bool far = std::is_same<E, I8>::value && __any(mine_sa > kFar);
 #pragma unroll
         for (int h = 0; h < 64 / kRows; ++h)
 #pragma unroll
@@ -415,7 +426,7 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
                 const uint32_t r = q + d * kDown + lane / kAcross;
                 const u4* const from = mine + r * (kWave / 4);
                 in[d][0] = from[lane % kAcross * 2 ^ (r & 15)], in[d][1] = from[(lane % kAcross * 2 + 1) ^ (r & 15)];
-                if constexpr (std::is_same<E, I8>::value) sa[d] = p.a_scales[min(t0 + r, at.end - 1)];
+                if constexpr (std::is_same<E, I8>::value) sa[d] = __shfl(mine_sa, (int)r);
             }
 #pragma unroll
             for (int d = 0; d < kDeep; ++d) {
@@ -431,9 +442,15 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
                 for (int j = 0; j < 8; ++j) {
                     const uint32_t u = in[d][j / 4][j % 4];
                     if constexpr (std::is_same<E, I8>::value)
-                        v[j] = scaled((int)u, sa[d], sw[j]);
+                        v[j] = (float)(int)u * sa[d] * sw[j];
                     else
                         v[j] = from_bits(u);
+                }
+                if constexpr (std::is_same<E, I8>::value) {
+                    if (far) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = scaled((int)in[d][j / 4][j % 4], sa[d], sw[j]);
+                    }
                 }
                 if (t >= at.end || count < 8) continue;
                 typename Out::Elem* const o = static_cast<typename Out::Elem*>(p.y) + t * p.y_stride + col;

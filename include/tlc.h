@@ -575,8 +575,8 @@ int tlc_q8_pack_columns(const void* x, uint64_t x_stride, int dtype, uint64_t ro
 /* y[t][o] = a_scales[t] * w_scales[o] * sum over c < k of a[t][c]*w[o][c]
  * (added to y[t][o] with accumulate != 0, fp32 only), a [rows, k] and w [n, k]
  * as above.  The sum is exact; its conversion to fp32 and the two products with
- * the scales, the smaller one first, are rounded, and the result is rounded to
- * y's dtype.  With offsets, rows are grouped by expert (below) and w holds
+ * the scales, a's first (w's where a's is above 2^96), are rounded, and the
+ * result is rounded to y's dtype.  With offsets, rows are grouped by expert (below) and w holds
  * experts*n rows, expert e's from e*n.
  * The workspace may be NULL where the size is 0. */
 size_t tlc_q8_product_workspace_size(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts);
