@@ -17,6 +17,7 @@ namespace {
 
 using namespace tlc_ckpt8;
 using namespace tlc_experts;
+using tlc_internal::launch;
 using tlc_internal::launch_blocks;
 
 constexpr int kThreads = 256;
@@ -44,6 +45,7 @@ struct ProductArgs {
     uint32_t* partial;                      // with several slices: their sums, [slices][rows][partial_row]
     uint32_t partial_row, slices, slice_k;  // n up to a multiple of 8; a slice's share of k, whole steps
     uint32_t tiles_n;
+    int tail;                               // a last round of few large tiles is left to, or is, smaller ones
     uint32_t first;                         // block of the whole that the launch begins with
 };
 
@@ -166,6 +168,19 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
+// Tile `b` of tiles_t by tiles_n: neighbours in bands of 4 tiles of rows.
+struct Place {
+    uint32_t t, n;
+};
+__device__ __forceinline__ Place place_of(uint32_t b, uint32_t tiles_t, uint32_t tiles_n) {
+    const uint32_t band = b / (4 * tiles_n), in_band = b % (4 * tiles_n), rows = min(4u, tiles_t - band * 4);
+    return {band * 4 + in_band % rows, in_band / rows};
+}
+
+// Of so many 256x256 tiles, those of the last round, where it is half empty or
+// more: another launch computes them in 128x128 tiles, which fill the chip.
+__host__ __device__ inline uint32_t tail_of(uint32_t tiles) { return tiles % 256 <= 128 ? tiles % 256 : 0; }
+
 // Inner weights of 16 bits: the 16-byte slots (8 columns) of row r lie at
 // slot ^ swizzle(r), so that what half a wavefront reads at once, 4 rows of 32
 // columns or 8 rows of 16, falls into the 64 banks once each.
@@ -208,18 +223,31 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void k_product(Prod
     };
     __shared__ Stage stage0, stage1;
 
-    uint32_t b = p.first + blockIdx.x;
-    const uint32_t tiles_t = tiles_of(p.experts, kTile), tiles = tiles_t * p.tiles_n, total = tiles * p.slices;
-    if (b >= total) return;
-    b = xcd_place(b, total);
-    const uint32_t slice = p.slices > 1 ? b / tiles : 0;
-    b -= slice * tiles;
-    // bands of 4 tiles of rows
-    const uint32_t band = b / (4 * p.tiles_n), in_band = b % (4 * p.tiles_n);
-    const uint32_t band_rows = min(4u, tiles_t - band * 4);
-    const Span at = tile_rows(p.experts, kTile, band * 4 + in_band % band_rows);
-    const uint32_t o0 = in_band / band_rows * kTile;
-    if (at.begin >= at.end) return;  // offsets that change meanwhile
+    uint32_t b = p.first + blockIdx.x, slice = 0;
+    Span at;
+    uint32_t o0;
+    if (kTile == 128 && p.tail) {
+        const uint32_t across = (p.n + 255) / 256, down = tiles_of(p.experts, 256), large = down * across;
+        const uint32_t rest = tail_of(large);
+        if (b >= rest * 4) return;
+        b = xcd_place(b, rest * 4);
+        const Place place = place_of(large - rest + b / 4, down, across);
+        at = tile_rows(p.experts, 256, place.t);
+        at.begin += b / 2 % 2 * 128;
+        at.end = min(at.end, at.begin + 128);
+        o0 = place.n * 256 + b % 2 * 128;
+        if (o0 >= p.n) return;
+    } else {
+        const uint32_t tiles_t = tiles_of(p.experts, kTile), tiles = tiles_t * p.tiles_n;
+        const uint32_t total = p.tail ? tiles - tail_of(tiles) : tiles * p.slices;
+        if (b >= total) return;
+        b = xcd_place(b, total);
+        if (p.slices > 1) slice = b / tiles, b -= slice * tiles;
+        const Place place = place_of(b, tiles_t, p.tiles_n);
+        at = tile_rows(p.experts, kTile, place.t);
+        o0 = place.n * kTile;
+    }
+    if (at.begin >= at.end) return;  // the lower half of a short tile, or offsets that change meanwhile
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const uint32_t k_first = slice * p.slice_k, k_here = min(p.k - k_first, p.slice_k);
@@ -679,10 +707,12 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool gro
             if (slices > 1 && steps < 4 * slices) break;
             const uint64_t share = (steps + slices - 1) / slices, cut = (steps + share - 1) / share;
             if (worst * ((n + tile - 1) / tile) * cut > 0xFFFFFFFFull) break;
-            const double blocks = std::max(1.0, tiles_t * (double)((n + tile - 1) / tile) * (double)cut);
+            const double blocks = std::max(1.0, std::ceil(tiles_t) * (double)((n + tile - 1) / tile) * (double)cut);
             double us;
             if (tile == 256) {
-                us = std::ceil(blocks / 256) * (1.55 * (double)share + 8.0);
+                const double rest = cut == 1 ? (double)tail_of((uint32_t)std::min(blocks, 4e9)) : 0.0;
+                us = std::ceil((blocks - rest) / 256) * (1.55 * (double)share + 8.0);
+                if (rest > 0.0) us += (rest <= 64 ? 0.5 : 1.0) * (double)share + 7.0;
             } else {
                 const double one = (size == 4 ? 2.0 : 0.5) * (double)share, two = (size == 4 ? 4.6 : 1.0) * (double)share;
                 const double full = std::floor(blocks / 512), rest = blocks - full * 512;
@@ -750,10 +780,20 @@ int product(const char* name, ProductArgs p, void* workspace, size_t workspace_b
         });
     };
     int rc = TLC_OK;
-    if constexpr (sizeof(Elem) == 4)
+    if constexpr (sizeof(Elem) == 4) {
         rc = go(Int<128>{});
-    else
-        rc = s.tile == 256 ? go(Int<256>{}) : go(Int<128>{});
+    } else if (s.tile == 128) {
+        rc = go(Int<128>{});
+    } else {
+        const uint64_t large = most_tiles(p.experts.rows, p.experts.count, 256, grouped) * ((p.n + 255) / 256);
+        p.tail = s.slices == 1 && (grouped || tail_of((uint32_t)large));
+        rc = go(Int<256>{});
+        if (!rc && p.tail)
+            rc = launch(name, st, [&] {
+                p.first = 0;
+                k_product<E, Out, kInner, 128><<<(uint32_t)std::min<uint64_t>(large, 128) * 4, kThreads, 0, st>>>(p);
+            });
+    }
     if (rc || s.slices == 1) return rc;
     p.tiles_n = (p.partial_row / 8 + 7) / 8;
     const uint64_t tiles_t = most_tiles(p.experts.rows, p.experts.count, 32, grouped);

@@ -594,7 +594,8 @@ int tlc_q8_product(const int8_t* a, const float* a_scales, uint64_t rows, const 
  * expert, which then has every row.
  * w is [experts][n][k], its rows w_stride and its experts w_expert_stride
  * elements apart (0 included: the same weight for all).  Matrices of one call
- * have one dtype; sums are fp32 in a fixed order and rounded to the dtype once.
+ * have one dtype; sums are fp32, in an order that the sizes and offsets fix, and
+ * rounded to the dtype once.
  * Outputs must not overlap inputs.  Strides, sizes and refusals as for the
  * checkpoints above; TLC_ERR_INVALID_ARG also for more than 2^24 tiles of
  * 128 x 128 (rows/128 + experts of them in the rows) and, in the first two

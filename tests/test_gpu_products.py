@@ -360,13 +360,18 @@ def test_long_reductions(tlc, k, dtype):
         assert torch.equal(y8[b:t].cpu(), (q[0][0][b:t].double() @ q[1][0][e * n:(e + 1) * n].double().t()).float())
 
 
-@pytest.mark.parametrize("pad", [0, 3])
-@pytest.mark.parametrize("k", [1096, 1027])
+# Rows of two experts in one round of large tiles, 240 of them, and in 272, whose last 16 smaller ones compute: with a
+# last tile of 4 rows, and of 156.
+LARGE = [[1700, 1900], [2460, 1540], [1540, 2460]]
+
+
+@pytest.mark.parametrize("counts", LARGE)
+@pytest.mark.parametrize("k,pad", [(1096, 0), (1096, 3), (1027, 3)])
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_large_ragged_products_of_whole_numbers_are_exact(tlc, dtype, k, pad):
+def test_large_ragged_products_of_whole_numbers_are_exact(tlc, dtype, k, pad, counts):
     """Sizes that take the larger tile (in 16 bits and 8), with a ragged last one in every direction."""
-    counts, n, before, behind = [1700, 1900], 4091, 3, 5
-    say(f"large products {dtype} k={k} pad={pad}")
+    n, before, behind = 4091, 3, 5
+    say(f"large products {dtype} k={k} pad={pad} {counts}")
     g = gen(k + pad)
     offsets, rows = offsets_of(counts, before), before + sum(counts) + behind
     off = offsets.cuda()
@@ -383,18 +388,19 @@ def test_large_ragged_products_of_whole_numbers_are_exact(tlc, dtype, k, pad):
             assert torch.equal(v[b:t], want), e
 
 
-def test_large_ragged_product8_is_exact(tlc):
-    counts, n, k = [1700, 1900], 4091, 2055
+@pytest.mark.parametrize("counts", LARGE)
+def test_large_ragged_product8_is_exact(tlc, counts):
+    n, k, rows = 4091, 2055, sum(counts)
     g = gen(21)
     off = offsets_of(counts).cuda()
-    a, w = [torch.randint(-80, 81, (r, k), generator=g).to(torch.int8) for r in (3600, 2 * n)]
+    a, w = [torch.randint(-80, 81, (r, k), generator=g).to(torch.int8) for r in (rows, 2 * n)]
     pads = torch.nn.functional.pad
     q = [tlc.Rows8(pads(c, (0, 2176 - k)).cuda(), torch.ones(c.shape[0], device="cuda"), k) for c in (a, w)]
     y = tlc.q8_product(*q, torch.float32, offsets=off)
     z = torch.zeros_like(y)
     tlc.q8_product(*q, torch.float32, offsets=off, y=z, accumulate=True)
     assert torch.equal(y, z)
-    for e, (b, t) in enumerate(ref.spans(off.tolist(), 3600)):
+    for e, (b, t) in enumerate(ref.spans(off.tolist(), rows)):
         want = a[b:t].cuda().float() @ w[e * n:(e + 1) * n].cuda().float().t()  # 2055 * 80 * 80 is below 2^24
         assert torch.equal(y[b:t], want), e
 
