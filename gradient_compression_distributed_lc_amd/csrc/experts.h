@@ -121,6 +121,14 @@ __device__ __forceinline__ uint32_t xcd_place(uint32_t b, uint32_t total) {
     return run + (i < per * 8 ? i % 8 * per + i / 8 : i);
 }
 
+// Block b's place among experts of `tiles` tiles each, whose times differ: every
+// XCD takes an eighth of each expert's tiles, neighbours, where they divide so.
+__device__ __forceinline__ uint32_t xcd_share(uint32_t b, uint32_t tiles) {
+    if (tiles % 8) return b;
+    const uint32_t per = tiles / 8, turn = b / 8;
+    return turn / per * tiles + b % 8 * per + turn % per;
+}
+
 // The most tiles that `rows` rows of `experts` experts can need.
 inline uint64_t most_tiles(uint64_t rows, uint64_t experts, uint64_t tile, bool grouped) {
     return grouped ? rows / tile + std::min(rows, experts) : (rows + tile - 1) / tile;
