@@ -181,10 +181,14 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
 
     // neighbouring tiles on one XCD: blocks go round the 8 of them. Experts' tiles
     // differ in time: in runs of neighbours an XCD gets the longest expert whole and
-    // works on alone, so each gets an eighth of every expert (against runs, 8 uneven
-    // experts of 5120x1280 over 16384 bf16 rows 401 -> 281 us, 16 of 1280x1280
-    // 111 -> 90, 4 of 1024x1024 79 -> 72, 8 of 4096x4096 within 2 % both ways, and
-    // in one short round, 5 experts of 1000x515 over 777 fp32 rows, 19.6 -> 21.1).
+    // works on alone, so each gets an eighth of every expert, and the longest expert
+    // is begun first. Runs, eighths, eighths with the longest first, us:
+    //   8 uneven experts of 5120x1280, 16384 bf16 rows   401  281  226 (dense 218)
+    //   16 of 1280x1280                                  111   90   69
+    //   32 of 1024x2048                                  176  147  132-140
+    //   64 of 1024x1024, 8192 rows                        98   87   89
+    //   8 of 4096x4096, 16384 rows: a round each         556  556  560
+    //   5 of 1000x515, 777 fp32 rows: one round           20   21   21
     uint32_t b = blockIdx.x;
     if constexpr (kExperts) {
         b = tlc_experts::xcd_share(b + p.first, p.tiles);
@@ -194,15 +198,16 @@ __global__ __launch_bounds__(kThreads * kGroups, 1) void k_weight_grad(MatArgs p
         b += p.first;
     }
     const uint32_t slice = b / (kExperts ? p.tiles_all : p.tiles), tile = b % p.tiles;
-    const uint32_t expert = kExperts ? b % p.tiles_all / p.tiles : 0;
     uint32_t tile_i, tile_c;
     tile_place(p, tile, &tile_i, &tile_c);
     const uint32_t i0 = tile_i * kTile, c0 = tile_c * kTile;
-    float* const dw = kExperts ? p.dw + expert * p.dw_expert : p.dw;
+    float* dw = p.dw;
     // the group's share of the slice's rows, the same steps for each group
     uint64_t s_begin, s_end;
     if constexpr (kExperts) {
-        const Span mine = tlc_experts::rows_of(p.experts, expert);
+        const Span mine = tlc_experts::rows_by_length(p.experts, b % p.tiles_all / p.tiles);
+        dw += mine.expert * p.dw_expert;
+        b = slice * p.tiles_all + mine.expert * p.tiles + tile;
         const uint64_t cut = ((mine.end - mine.begin + p.slices - 1) / p.slices + 63) / 64 * 64;
         s_begin = min(mine.begin + slice * cut, (uint64_t)mine.end), s_end = min(s_begin + cut, (uint64_t)mine.end);
     } else {

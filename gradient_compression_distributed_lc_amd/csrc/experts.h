@@ -114,6 +114,23 @@ __device__ __forceinline__ Span rows_of(const Experts& x, uint32_t expert) {
     return s;
 }
 
+// All rows of the expert whose turn it is: the longest first, of equally long
+// ones the first, so that no long expert is begun when the others end. More than
+// 64 experts, whose lengths one wavefront does not hold at once, come in order.
+__device__ __forceinline__ Span rows_by_length(const Experts& x, uint32_t turn) {
+    if (!x.offsets || x.count > 64) return rows_of(x, turn);
+    uint32_t b, e, before = 0, rank = 0;
+    spans(x, 0, &before, &b, &e);
+    // different for every lane, least for those past the last expert
+    const uint32_t key = min(e - b, (1u << 26) - 1) << 6 | (63 - (threadIdx.x & 63));
+    for (uint32_t i = 0; i < x.count; i += 8)
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)key, (int)(i + j)) > key;
+    const int at = __builtin_ctzll(__ballot(rank == turn));  // a rank is one lane's
+    return {(uint32_t)at, (uint32_t)__builtin_amdgcn_readlane((int)b, at),
+            (uint32_t)__builtin_amdgcn_readlane((int)e, at)};
+}
+
 // Block b's place among `total`: blocks go round the 8 XCDs, and of each 256
 // blocks, which run at about the same time, an XCD takes neighbours.
 __device__ __forceinline__ uint32_t xcd_place(uint32_t b, uint32_t total) {

@@ -493,6 +493,28 @@ def test_expert_weight_gradient_of_many_tiles_and_slices(tlc, dtype):
             assert torch.equal(dw[e], want), (counts, e)
 
 
+@pytest.mark.parametrize("n,cols", [(256, 512), (200, 300)])
+@pytest.mark.parametrize("experts", [7, 8, 9, 63, 64, 65])
+def test_expert_weight_gradient_in_any_order_of_lengths(tlc, experts, n, cols):
+    """Longest first, up to a wavefront's lanes of experts: rising, falling, equal, all but one empty, and offsets that turn back."""
+    say(f"expert weight grad order {experts} {n} {cols}")
+    g = gen(experts)
+    e = list(range(experts))
+    one = [0] * experts
+    one[experts // 2] = 333
+    turning = offsets_of([5] * experts)
+    turning[experts // 3] = 2**63 - 1 if experts % 2 else 0  # past the rows, or back to the first
+    for offsets in [offsets_of(c) for c in (e, e[::-1], [17] * experts, one)] + [turning]:
+        rows = max(int(offsets[-1]), 1)
+        dy, x = whole(g, rows, n, dtype=torch.bfloat16), whole(g, rows, cols)
+        codes, scales = ckpt8_ref.encode(x, ckpt8_ref.INT8)
+        x8 = tlc.Checkpoint8(codes.cuda(), scales.cuda(), cols, ckpt8_ref.INT8)
+        dw = tlc.expert_weight_grad(dy.cuda(), x8, offsets.cuda())
+        for i, (b, t) in enumerate(ref.spans(offsets.tolist(), rows)):
+            # whole numbers of at most 2^24: exact in fp32
+            assert torch.equal(dw[i], dy[b:t].cuda().float().t() @ x[b:t].cuda()), (offsets, i)
+
+
 def test_no_rows(tlc):
     off = torch.zeros(4, dtype=torch.int64, device="cuda")
     w = torch.ones(3, 8, 16, dtype=torch.bfloat16, device="cuda")
