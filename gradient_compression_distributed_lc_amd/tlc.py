@@ -1191,11 +1191,13 @@ def _result(out: torch.Tensor | None, name: str, rows: int, cols: int, dtype: to
 
 
 def _product_workspace(nbytes: int, device, workspace):
-    """(pointer, bytes) of a workspace that may need nothing."""
+    """(workspace, pointer, bytes), nothing where nothing is needed.  The caller
+    holds the workspace until the launch: another thread's call on the stream
+    could be given its memory in between."""
     if nbytes == 0 and workspace is None:
-        return None, 0
+        return None, None, 0
     ws = _ckpt8_workspace(nbytes, device, workspace)
-    return ws.data_ptr(), ws.numel()
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def q8_pack_rows(x: torch.Tensor, *, out: Rows8 | None = None, stream=None) -> Rows8:
@@ -1256,7 +1258,7 @@ def q8_product(a: Rows8, w: Rows8, dtype: torch.dtype = torch.bfloat16, *, offse
 
     def body(st):
         o, py, sy = _result(y, "y", rows, n, dtype, device)
-        pws, nws = _product_workspace(q8_product_workspace_size(rows, n, k, experts), device, workspace)
+        ws, pws, nws = _product_workspace(q8_product_workspace_size(rows, n, k, experts), device, workspace)
         _check(lib().tlc_q8_product(pa, psa, rows, pw, psw, n, k, po, experts, py, sy, _DTYPES[dtype],
                                     int(accumulate), pws, nws, st), "tlc_q8_product")
         return o
@@ -1285,7 +1287,8 @@ def expert_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | Non
 
     def body(st):
         o, py, sy = _result(y, "y", rows, n, x.dtype, device)
-        pws, nws = _product_workspace(expert_product_workspace_size(rows, k, n, experts, x.dtype), device, workspace)
+        ws, pws, nws = _product_workspace(expert_product_workspace_size(rows, k, n, experts, x.dtype), device,
+                                          workspace)
         _check(lib().tlc_expert_product(px, sx, _DTYPES[x.dtype], rows, k, pw, sw, se, n, pf, experts, py, sy, pws,
                                         nws, st), "tlc_expert_product")
         return o
@@ -1312,8 +1315,8 @@ def expert_input_grad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor |
 
     def body(st):
         o, po, so = _result(dx, "dx", rows, k, dy.dtype, device)
-        pws, nws = _product_workspace(expert_input_grad_workspace_size(rows, n, k, experts, dy.dtype), device,
-                                      workspace)
+        ws, pws, nws = _product_workspace(expert_input_grad_workspace_size(rows, n, k, experts, dy.dtype), device,
+                                          workspace)
         _check(lib().tlc_expert_input_grad(pd, sd, _DTYPES[dy.dtype], rows, n, pw, sw, se, k, pf, experts, po, so, pws,
                                            nws, st), "tlc_expert_input_grad")
         return o

@@ -3,6 +3,7 @@ chip is full and the sizes are awkward: many blocks of the kernel for few rows,
 sums in slices that are added to, scales at the ends of the range in every
 kernel, the larger tile without offsets, thousands of experts, calls at once."""
 import math
+import weakref
 
 import pytest
 import torch
@@ -88,3 +89,42 @@ def test_step_of_many_uneven_experts(tlc, dtype, experts, k, n, seed):
                 # up to three numbers in the last, whose products are exact
                 bound = 2 * terms * 2.0 ** -24 * size + U[out] * want.abs() * 1.01 + LEAST[out]
                 assert_close(got, want, bound, (name, e, rows))
+
+
+# ---- workspaces --------------------------------------------------------------
+
+
+def test_workspace_lives_until_the_call_is_launched(tlc, monkeypatch):
+    """A call's own workspace is not given back before its kernels are launched: another thread's call on the same stream
+    could be given it in between, and its results be written over."""
+    rows, k, n = 128, 4096, 256
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, n, k, dtype=torch.bfloat16, device="cuda")
+    a8, w8 = tlc.q8_pack_rows(x), tlc.q8_pack_rows(w[0])
+    assert tlc.expert_product_workspace_size(rows, k, n, 1, x.dtype) and tlc.q8_product_workspace_size(rows, n, k)
+    assert tlc.expert_input_grad_workspace_size(rows, k, n, 1, x.dtype)
+    real, made, seen = tlc.lib(), [], []
+    make = tlc._ckpt8_workspace
+
+    def made_and_watched(nbytes, device, workspace):
+        t = make(nbytes, device, workspace)
+        made.append(weakref.ref(t))
+        return t
+
+    class Watch:
+        def __getattr__(self, name):
+            f = getattr(real, name)
+
+            def call(*args):
+                if not name.endswith("_size"):
+                    seen.append((name, made[-1]() is not None))
+                return f(*args)
+            return call
+
+    monkeypatch.setattr(tlc, "_ckpt8_workspace", made_and_watched)
+    monkeypatch.setattr(tlc, "lib", lambda: Watch())
+    tlc.expert_product(x, w)
+    tlc.expert_input_grad(x, w.transpose(1, 2).contiguous())
+    tlc.q8_product(a8, w8)
+    torch.cuda.synchronize()
+    assert seen == [("tlc_expert_product", True), ("tlc_expert_input_grad", True), ("tlc_q8_product", True)]
