@@ -11,7 +11,8 @@ import torch
 import ckpt8_ref
 import products_ref as ref
 from gpu_util import say
-from test_gpu_products import DTYPES, LEAST, U, assert_close, gen, offsets_of, randn, strided, whole
+from test_gpu_products import (DTYPES, LEAST, U, assert_close, gen, offsets_of, randn, random_codes, rows8, strided,
+                               whole)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,147 @@ def test_workspace_lives_until_the_call_is_launched(tlc, monkeypatch):
     tlc.q8_product(a8, w8)
     torch.cuda.synchronize()
     assert seen == [("tlc_expert_product", True), ("tlc_expert_input_grad", True), ("tlc_q8_product", True)]
+
+
+# ---- sums in slices ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,n,k", [(140, 77, 8191), (768, 768, 4096), (43, 1000, 20000)])
+@pytest.mark.parametrize("experts", [0, 3])
+def test_product8_in_slices_added_to_a_bucket(tlc, experts, rows, n, k):
+    """Reductions cut into slices, whose sums are added to a strided place of whole numbers."""
+    say(f"product8 in slices, added {rows}x{n}x{k} {experts}")
+    many = max(experts, 1)
+    assert tlc.q8_product_workspace_size(rows, n, k, many) > 0
+    g = gen(rows + k)
+    (a, _), (w, _) = random_codes(g, rows, k), random_codes(g, many * n, k)
+    sa, sw = torch.ones(rows), torch.ones(many * n)
+    offsets = offsets_of([rows - rows // 3, 0, rows // 3 - 2], 1) if experts else torch.tensor([0, rows])
+    start = whole(g, rows, n, most=1000)
+    want = start.double()
+    for e, (b, t) in enumerate(ref.spans(offsets.tolist(), rows)):
+        sums = a[b:t].float().cuda() @ w[e * n:(e + 1) * n].float().cuda().t()  # below 2^24: exact
+        assert sums.numel() == 0 or sums.abs().max() < 2 ** 23
+        want[b:t] += sums.cpu().double()
+    bucket = strided(start, 3, 2)
+    off = offsets.cuda() if experts else None
+    y = tlc.q8_product(rows8(tlc, a, sa, k), rows8(tlc, w, sw, k), torch.float32, offsets=off, y=bucket,
+                       accumulate=True)
+    assert y is bucket and torch.equal(y.cpu().double(), want)
+    assert torch.isnan(torch.as_strided(bucket, (rows, 3), (n + 3, 1), bucket.storage_offset() + n)).all()
+
+
+def test_a_smaller_batch_may_need_a_larger_workspace(tlc):
+    """A workspace that holds for many rows can be too small for fewer, whose reduction is cut: the call is refused, and
+    the size for just these rows is taken."""
+    k = n = 4096
+    sizes = {r: tlc.expert_product_workspace_size(r, k, n, 1, torch.bfloat16) for r in (1024, 4096)}
+    assert sizes[1024] > sizes[4096] == 0
+    x = whole(gen(2), 1024, k, dtype=torch.bfloat16, most=1).cuda()
+    w = whole(gen(3), 1, n, k, dtype=torch.bfloat16, most=1).cuda()
+    off = offsets_of([1024]).cuda()
+    with pytest.raises(tlc.TLCError):
+        tlc.expert_product(x, w, off, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    y = tlc.expert_product(x, w, off, workspace=torch.empty(sizes[1024], dtype=torch.uint8, device="cuda"))
+    assert torch.equal(y, (x.float() @ w[0].float().t()).bfloat16())
+
+
+# ---- scales ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows,n,k", [(7, 203, 64), (200, 203, 64), (140, 77, 8191), (700, 520, 300)])
+def test_product8_scales_of_every_size_side_by_side(tlc, rows, n, k):
+    """Scales from 2^-126 to 2^121 and NaN next to each other in a wavefront's rows and columns, in the kernels for few
+    rows, for tiles with a ragged end and for slices.  Scales are powers of two and sums below 2^24, so one rounding at
+    most, to a subnormal value, is what the result differs by from the exact one."""
+    say(f"product8 scales {rows}x{n}x{k}")
+    g = gen(rows + n)
+    a, w = torch.zeros(rows, -(-k // 128) * 128, dtype=torch.int8), torch.zeros(n, -(-k // 128) * 128, dtype=torch.int8)
+    a[:, :k], w[:, :k] = whole(g, rows, k).to(torch.int8), whole(g, n, k).to(torch.int8)
+    exponents = torch.tensor([-126, -100, -20, 0, 5, 60, 96, 97, 120, 121])
+    sa = torch.ldexp(torch.ones(rows), exponents[torch.randint(0, 10, (rows,), generator=g)])
+    sw = torch.ldexp(torch.ones(n), exponents[torch.randint(0, 10, (n,), generator=g)])
+    sa[3], sw[n - 2], sw[5] = math.nan, math.nan, math.nan
+    want, sums = ref.product8(a, sa, w, sw)
+    assert sums.abs().max() < 2 ** 24
+    want = want.float()
+    assert torch.isinf(want).any() and (want.abs() < 2.0 ** -126).any() and torch.isfinite(want).any()
+    for add in (False, True):
+        start = whole(g, rows, n, most=1000)
+        y = strided(start, 1, 1)
+        tlc.q8_product(rows8(tlc, a, sa, k), rows8(tlc, w, sw, k), torch.float32, y=y, accumulate=add)
+        assert torch.equal(torch.nan_to_num(y.cpu(), nan=7.5, posinf=8.5, neginf=9.5),
+                           torch.nan_to_num(want + start if add else want, nan=7.5, posinf=8.5, neginf=9.5)), add
+
+
+# ---- the larger tile without offsets -----------------------------------------
+
+
+@pytest.mark.parametrize("rows", [4008, 4264])
+@pytest.mark.parametrize("k", [1096, 1027])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_large_dense_products_of_whole_numbers_are_exact(tlc, dtype, k, rows):
+    """256 large tiles in one round, and 272, whose last 16 smaller ones compute, the host deciding."""
+    say(f"large dense products {rows} {k} {dtype}")
+    n = 4091
+    g = gen(k + rows)
+    x, w = whole(g, rows, k, dtype=dtype).cuda(), whole(g, 1, n, k, dtype=dtype).cuda()
+    want = (x.float() @ w[0].float().t()).to(dtype)  # whole numbers below 2^24
+    assert torch.equal(tlc.expert_product(x, w), want)
+    assert torch.equal(tlc.expert_input_grad(x, w.transpose(1, 2).contiguous()), want)
+    z = strided(torch.full((rows, n), math.nan, dtype=dtype), 3, 1)
+    tlc.expert_product(strided(x.cpu(), 5, 1), strided(w.cpu(), 3), y=z)
+    assert torch.equal(z, want)
+
+
+@pytest.mark.parametrize("rows", [4008, 4264])
+def test_large_dense_product8_is_exact(tlc, rows):
+    n, k = 4091, 2055
+    g = gen(rows)
+    a, w = torch.zeros(rows, 2176, dtype=torch.int8), torch.zeros(n, 2176, dtype=torch.int8)
+    a[:, :k] = torch.randint(-80, 81, (rows, k), generator=g).to(torch.int8)
+    w[:, :k] = torch.randint(-80, 81, (n, k), generator=g).to(torch.int8)
+    sa = torch.ldexp(torch.ones(rows), torch.randint(-3, 4, (rows,), generator=g))
+    sa[70::128] = 2.0 ** 97  # with a scale that reverses the order of the products
+    sw = torch.ldexp(torch.ones(n), torch.randint(-3, 4, (n,), generator=g))
+    want = (a.cuda().float() @ w.cuda().float().t()) * sa.cuda()[:, None] * sw.cuda()  # 2055 * 80 * 80 is below 2^24
+    assert torch.equal(tlc.q8_product(rows8(tlc, a, sa, k), rows8(tlc, w, sw, k), torch.float32), want)
+
+
+# ---- thousands of experts ----------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts", [1000, 65536])
+@pytest.mark.parametrize("k,n,rows", [(40, 24, 3000), (3, 8, 300), (136, 8, 20000)])
+def test_thousands_of_experts(tlc, k, n, rows, experts, dtype):
+    """Up to as many experts as the calls take: whole numbers, so exact."""
+    say(f"thousands of experts {experts} {k} {n} {rows} {dtype}")
+    g = gen(experts + k)
+    who = torch.sort(torch.randint(0, experts, (rows,), generator=g)).values
+    who[: rows // 3] = who[rows // 3]  # a long one, the first with rows
+    offsets = torch.searchsorted(who, torch.arange(experts + 1)).cuda()
+    who = who.cuda()
+    x, dy = whole(g, rows, k, dtype=dtype).cuda(), whole(g, rows, n, dtype=dtype).cuda()
+    w = torch.randint(-3, 4, (experts, n, k), device="cuda").to(dtype)
+    y, dx = tlc.expert_product(x, w, offsets), tlc.expert_input_grad(dy, w, offsets)
+    x8 = tlc.ckpt8_pack(x, ckpt8_ref.INT8)
+    dw = tlc.expert_weight_grad(dy, x8, offsets)
+    q = tlc.q8_pack_rows(x), tlc.q8_pack_rows(w.view(experts * n, k))
+    y8 = tlc.q8_product(*q, torch.float32, offsets=offsets)
+    for b in range(0, rows, 1000):
+        some = slice(b, b + 1000)
+        we, xs, ds = w[who[some]].float(), x[some].float(), dy[some].float()
+        assert torch.equal(y[some], (we * xs[:, None, :]).sum(2).to(dtype))
+        assert torch.equal(dx[some], (we * ds[:, :, None]).sum(1).to(dtype))
+        codes = q[1].codes.view(experts, n, -1)[who[some]].float() * q[0].codes[some].float()[:, None, :]
+        scales = q[0].scales[some][:, None] * q[1].scales.view(experts, n)[who[some]]
+        # the sum's conversion is exact here, the two products with the scales round, in either order
+        assert ((y8[some] - codes.sum(2) * scales).abs() <= 4 * 2.0 ** -24 * (codes.sum(2) * scales).abs()).all()
+    ends = offsets.tolist()
+    some = sorted({0, 1, experts - 1, int(who[0]), *who[:: max(1, rows // 50)].tolist()})
+    for e in some:
+        b, t = ends[e], ends[e + 1]
+        assert torch.equal(dw[e], dy[b:t].float().t() @ x[b:t].float()), e
+    empty = offsets[1:] == offsets[:-1]
+    assert not dw[empty].any()
