@@ -6,7 +6,7 @@
 // row of either side.  16-bit and fp32 sums are the matrix cores' fp32, integer
 // sums are exact in 32 bits.
 #include <algorithm>
-#include <numeric>
+#include <cmath>
 #include <type_traits>
 
 #include "ckpt8.h"
@@ -24,7 +24,6 @@ constexpr int kThreads = 256;
 
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
-typedef int i16v __attribute__((ext_vector_type(16)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b8v __attribute__((ext_vector_type(8)));
 typedef _Float16 h8v __attribute__((ext_vector_type(8)));
@@ -50,25 +49,22 @@ struct ProductArgs {
 };
 
 // A product of kRows rows by kRows rows, 32 over 32 bytes of the reduction or 16
-// over 64: a lane holds 16 bytes of row lane%kRows on either side, which ones by
-// lane/kRows.
+// over 64 (8 bits: 16 only): a lane holds 16 bytes of row lane%kRows on either
+// side, which ones by lane/kRows.
 template <typename E, int kRows>
 struct Sums {
     using Type = typename std::conditional<kRows == 32, f16v, f4>::type;
 };
-template <int kRows>
-struct Sums<I8, kRows> {
-    using Type = typename std::conditional<kRows == 32, i16v, i4>::type;
+template <>
+struct Sums<I8, 16> {
+    using Type = i4;
 };
 template <typename E, int kRows, typename Sum = typename Sums<E, kRows>::Type>
 __device__ __forceinline__ Sum multiply(u4 a, u4 b, Sum c) {
     constexpr bool k32 = kRows == 32;
     if constexpr (std::is_same<E, I8>::value) {
-        const i4 x = __builtin_bit_cast(i4, a), y = __builtin_bit_cast(i4, b);
-        if constexpr (k32)
-            return __builtin_amdgcn_mfma_i32_32x32x32_i8(x, y, c, 0, 0, 0);
-        else
-            return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, c, 0, 0, 0);
+        static_assert(!k32, "8 bits multiply 16 rows");
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, a), __builtin_bit_cast(i4, b), c, 0, 0, 0);
     } else if constexpr (std::is_same<E, BF16>::value) {
         const b8v x = __builtin_bit_cast(b8v, a), y = __builtin_bit_cast(b8v, b);
         if constexpr (k32)
