@@ -1117,6 +1117,7 @@ def ckpt8_weight_grad(dy: torch.Tensor, x: Checkpoint8, *, col_scale: torch.Tens
 class Rows8:
     """A matrix [rows, cols] in 8-bit integers with one scale per row (layout in
     tlc.h): value [r, c] is codes[r, c] * scales[r], codes past cols are 0.
+    Codes made elsewhere are -127 to 127, or -128 too with cols below 131072.
     Rows can be sliced off as ``Rows8(q.codes[a:b], q.scales[a:b], q.cols)``."""
     codes: torch.Tensor   # int8[rows, 128*ceil(cols/128)]
     scales: torch.Tensor  # float32[rows]

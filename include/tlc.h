@@ -452,7 +452,10 @@ int tlc_planes_scatter(const float* src, const uint64_t* src_off, float* dst, co
  * beside the type's rounding).  Outputs must not overlap inputs or each
  * other unless said otherwise.  No call here has a status word: nothing in the
  * data can be refused.  Workspaces as above (device, 256-byte aligned, size
- * from the *_workspace_size call, host only, 0 for sizes out of range). */
+ * from the *_workspace_size call, host only, 0 for sizes out of range).  A size
+ * is that of a call with just these arguments: fewer rows can need more than
+ * many, since a long reduction is cut where there are few tiles, so a workspace
+ * kept for varying rows has to hold the largest of their sizes. */
 enum tlc_dtype { TLC_F32 = 0, TLC_F16 = 1, TLC_BF16 = 2 };
 enum tlc_ckpt8_format { TLC_CKPT8_INT8 = 1, TLC_CKPT8_E4M3 = 2 };
 /* f(x): x*Phi(x); its form with tanh(sqrt(2/pi)*(x + 0.044715 x^3)); x/(1+e^-x) */
@@ -556,7 +559,8 @@ int tlc_ckpt8_weight_grad(const void* dy, uint64_t dy_stride, int dtype, uint64_
  *   dx = dy W:     rows of dy    by columns of W;
  *   dW = dy^T x:   columns of dy by columns of x, fp32, into a gradient bucket.
  * Strides, dtypes, sizes and refusals as for the checkpoints above, and
- * cols <= 131072, so that sums of products stay in 32 bits. */
+ * cols <= 131072, so that sums of products stay in 32 bits: codes are -127 to
+ * 127, and a caller's own may be -128 too where cols < 131072. */
 
 /* Bytes between the rows of codes: a multiple of 128.  0 for cols out of range. */
 uint64_t tlc_q8_code_stride(uint64_t cols);
@@ -574,7 +578,7 @@ int tlc_q8_pack_columns(const void* x, uint64_t x_stride, int dtype, uint64_t ro
 
 /* y[t][o] = a_scales[t] * w_scales[o] * sum over c < k of a[t][c]*w[o][c]
  * (added to y[t][o] with accumulate != 0, fp32 only), a [rows, k] and w [n, k]
- * as above.  The sum is exact; its conversion to fp32 and the two products with
+ * as above.  The sum of such codes is exact; its conversion to fp32 and the two products with
  * the scales, a's first (w's where a's is above 2^96), are rounded, and the
  * result is rounded to y's dtype.  With offsets, rows are grouped by expert (below) and w holds
  * experts*n rows, expert e's from e*n.

@@ -174,7 +174,24 @@ def test_a_smaller_batch_may_need_a_larger_workspace(tlc):
     assert torch.equal(y, (x.float() @ w[0].float().t()).bfloat16())
 
 
-# ---- scales ------------------------------------------------------------------
+# ---- codes and scales --------------------------------------------------------
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_product8_of_codes_of_the_least_value(tlc, rows):
+    """-128 by -128 over 131071: 2^31 less 2^14, the largest sum there is, exact before it is rounded to fp32."""
+    k = 131071
+    a, w = torch.full((rows, 131072), -128, dtype=torch.int8), torch.full((40, 131072), -128, dtype=torch.int8)
+    a[:, k:], w[:, k:] = 0, 0
+    a[1], w[7, ::3] = 127, 126
+    a[1, k:] = 0
+    w[7, k:] = 0
+    one = torch.ones
+    want = a.double() @ w.double().t()
+    assert want.max() == 2 ** 31 - 2 ** 14
+    y = tlc.q8_product(rows8(tlc, a, one(rows), k), rows8(tlc, w, one(40), k), torch.float32)
+    assert torch.equal(y.cpu(), want.float())
+
 
 
 @pytest.mark.parametrize("rows,n,k", [(7, 203, 64), (200, 203, 64), (140, 77, 8191), (700, 520, 300)])
