@@ -680,11 +680,13 @@ __global__ __launch_bounds__(kThreads) void k_product_narrow(ProductArgs p, uint
 
 // The tile and the slices of the reduction, by the least of an estimate in
 // microseconds.  Measured, in steps of 128 bytes: a 128x128 tile takes 0.5 us a
-// step alone on a CU, two at once 1.0, a 256x256 tile 1.5 (8 bits 1.8), in 16
-// bits and in 8 (fp32, in the smaller tile only: 2.0 and 4.6); a tile's beginning
-// and end take 4 and 8 us.  Slices fill the chip where the tiles do not and cost writing and
-// reading their sums.  Rows of experts are taken as equally many: half a tile
-// more for each.
+// step alone on a CU, two at once 1.0, a 256x256 tile 1.4 to 1.6 by the power
+// that the whole call draws (one round of 4096x4096 1.38 to 1.46, eight rounds of
+// 16384x8192x8192 1.49 in bf16 and 1.61 in 8 bits; taken as 1.55), in 16 bits
+// and in 8 (fp32, in the smaller tile only: 2.0 and 4.6); a tile's beginning and
+// end take 4 and 8 us.  Slices fill the chip where the tiles do not and cost
+// writing and reading their sums.  Rows of experts are taken as equally many:
+// half a tile more for each.
 //   bf16, tiles of 128 and 256 in one slice, and the best in slices, us:
 //   16384x4096x4096   504  407
 //   4096x4096x1024     42   36
@@ -728,9 +730,8 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool gro
 }
 
 // Whether rows are so few that w's bytes alone count: 8 to an expert on average
-// and 16 more, in fp32, whose larger tile is slow, 32 to an expert.  Rows may all
-// be one expert's, whose weight is then read once for each 16 of them, so no
-// more than where both measured the same.  Kernels for few rows and for tiles
+// and 16 more, in fp32, whose tile is slow, 32 to an expert, which is where both
+// measured the same for rows spread evenly.  Kernels for few rows and for tiles
 // (with slices), us with the launch, in 8 bits, bf16 and fp32:
 //   1 expert of 4096x4096, 16 rows    9, 12, 25 and 16, 19, 51
 //                          32 rows   12, 19, 38 and 17, 18, 51
@@ -738,6 +739,11 @@ Shape shape_of(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts, bool gro
 //   16 of 2048x4096, 4 rows each     39, 60, 138 and 54, 82, 368
 //                    16 rows each    48, 83, 165 and 44, 82, 348
 //   32 of 1024x2048, 32 rows each    49, 74, 144 and 24, 41, 175
+// What that rule does not see, since the host does not: rows that are nearly all
+// one expert's, whose weight is then read once for each 16 of them.  All on one:
+//   64 of 4096x4096, 528 rows        147 and 259 us in 8 bits and bf16, in tiles 23 and 35
+//                                    (spread evenly 260 and 466, in tiles 262 and 490)
+//   32 of 2048x2048, 1024 rows       238 in fp32, in tiles 77 (spread evenly 265)
 bool few(uint64_t rows, uint64_t experts, int size) { return rows <= (size == 4 ? 32 * experts : 8 * experts + 16); }
 
 uint64_t partial_row(uint64_t n) { return (n + 7) / 8 * 8; }
@@ -806,7 +812,7 @@ int product(const char* name, ProductArgs p, void* workspace, size_t workspace_b
 }
 
 constexpr uint64_t kMaxTiles = 1u << 24;   // of 128 x 128
-constexpr uint64_t kMaxStride = 1u << 22;  // a tile's 256 rows of fp32 lie within 32 bits
+constexpr uint64_t kMaxStride = 1u << 22;  // a tile's rows, 256 of 16 bits or 128 of fp32, lie within 2^31 bytes
 
 bool valid_product(uint64_t rows, uint64_t n, uint64_t k, uint64_t experts) {
     return valid_shape(rows, n) && k >= 1 && k <= kMaxDim && experts >= 1 && experts <= kMaxExperts &&
