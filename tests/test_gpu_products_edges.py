@@ -3,6 +3,7 @@ chip is full and the sizes are awkward: many blocks of the kernel for few rows,
 sums in slices that are added to, scales at the ends of the range in every
 kernel, the larger tile without offsets, thousands of experts, calls at once."""
 import math
+import threading
 import weakref
 
 import pytest
@@ -290,3 +291,100 @@ def test_thousands_of_experts(tlc, k, n, rows, experts, dtype):
         assert torch.equal(dw[e], dy[b:t].float().t() @ x[b:t].float()), e
     empty = offsets[1:] == offsets[:-1]
     assert not dw[empty].any()
+
+
+# ---- weight gradients --------------------------------------------------------
+
+
+@pytest.mark.parametrize("fmt", [ckpt8_ref.INT8, ckpt8_ref.E4M3])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_expert_weight_gradient_in_slices_added_to_a_bucket(tlc, dtype, fmt):
+    """Small weights over many rows, whose sums over slices of the rows are added to a strided place."""
+    counts, n, cols = [5000, 0, 9001], 130, 77
+    assert tlc.expert_weight_grad_workspace_size(sum(counts) + 3, n, cols, 3) > 256
+    g = gen(12)
+    offsets, rows = offsets_of(counts, 1), sum(counts) + 3
+    dy, x = whole(g, rows, n, dtype=dtype, most=2), whole(g, rows, cols, most=2)
+    codes, scales = ckpt8_ref.encode(x, fmt)
+    x8 = tlc.Checkpoint8(codes.cuda(), scales.cuda(), cols, fmt)
+    start = whole(g, 3, n, cols, most=50)
+    bucket = strided(start, 3, 2)
+    tlc.expert_weight_grad(strided(dy, 1, 1), x8, offsets.cuda(), dw=bucket, accumulate=True)
+    for e, (b, t) in enumerate(ref.spans(offsets.tolist(), rows)):
+        assert torch.equal(bucket[e].cpu(), start[e] + dy[b:t].float().t() @ x[b:t]), e  # below 2^24: exact
+    gaps = torch.as_strided(bucket, (3 * n, 3), (cols + 3, 1), bucket.storage_offset() + cols)
+    assert torch.isnan(gaps).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_expert_weight_gradient_of_values_that_are_not_finite(tlc, dtype):
+    """An infinity or NaN of a row reaches its own expert's gradient only, in the row of dw or the column that it is in;
+    rows of no expert are not read."""
+    n, cols, counts = 70, 100, [40, 0, 65, 31]
+    g = gen(13)
+    offsets, rows = offsets_of(counts, 2), sum(counts) + 5
+    dy, x = whole(g, rows, n, dtype=dtype), whole(g, rows, cols)
+    dy[0], dy[1], dy[-3:], x[0], x[-2:] = math.nan, math.inf, math.nan, math.nan, math.inf
+    dy[2 + 39, 7], dy[2 + 40, 8], x[2 + 39, 70] = math.inf, math.nan, math.nan  # the first's last row, the third's first
+    codes, scales = ckpt8_ref.encode(x, ckpt8_ref.INT8)
+    x8 = tlc.Checkpoint8(codes.cuda(), scales.cuda(), cols, ckpt8_ref.INT8)
+    dw = tlc.expert_weight_grad(dy.cuda(), x8, offsets.cuda()).cpu()
+    bad = torch.zeros(4, n, cols, dtype=torch.bool)
+    bad[0, 7], bad[2, 8] = True, True
+    bad[0, :, 64:96] = True  # the group of 32 columns that has no scale
+    assert not torch.isfinite(dw[bad]).any() and torch.isfinite(dw[~bad]).all()
+    for e, (b, t) in enumerate(ref.spans(offsets.tolist(), rows)):
+        want = dy[b:t].float().t() @ x[b:t]
+        assert torch.equal(dw[e][~bad[e]], want[~bad[e]]), e
+
+
+@pytest.mark.parametrize("rows,n,cols", [(333, 1000, 515), (5000, 128, 96)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_one_expert_without_offsets_is_the_dense_gradient(tlc, dtype, rows, n, cols):
+    g = gen(14)
+    dy, x = randn(g, rows, n, dtype=dtype).cuda(), randn(g, rows, cols, dtype=dtype).cuda()
+    x8 = tlc.ckpt8_pack(x, ckpt8_ref.E4M3)
+    dense = tlc.ckpt8_weight_grad(dy, x8)
+    assert torch.equal(tlc.expert_weight_grad(dy, x8)[0], dense)
+    # with offsets the rows are cut alike, at places that the device finds
+    assert torch.equal(tlc.expert_weight_grad(dy, x8, offsets_of([rows]).cuda())[0], dense)
+
+
+# ---- calls at once -----------------------------------------------------------
+
+
+def test_calls_of_two_threads_at_once(tlc):
+    """Two host threads, on one stream and on one of their own each: every result is that of a call alone."""
+    g = gen(15)
+    counts, k, n = [100, 0, 50, 6], 2048, 264
+    off, w = offsets_of(counts).cuda(), randn(g, 4, n, k, dtype=torch.bfloat16, scale=k ** -0.5).cuda()
+    assert tlc.expert_product_workspace_size(156, k, n, 4, w.dtype) > 0
+    xs = [randn(g, 156, k, dtype=torch.bfloat16).cuda() for _ in range(2)]
+    ds = [randn(g, 156, n, dtype=torch.bfloat16).cuda() for _ in range(2)]
+
+    def calls(i, stream):
+        return [tlc.expert_product(xs[i], w, off, stream=stream), tlc.expert_input_grad(ds[i], w, off, stream=stream),
+                tlc.expert_weight_grad(ds[i], tlc.ckpt8_pack(xs[i], ckpt8_ref.INT8, stream=stream), off, stream=stream),
+                tlc.q8_product(tlc.q8_pack_rows(xs[i], stream=stream), tlc.q8_pack_rows(xs[1 - i], stream=stream),
+                               stream=stream)]
+
+    want = [calls(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    one = torch.cuda.Stream()
+    for streams in ((one, one), (torch.cuda.Stream(), torch.cuda.Stream())):
+        got = [[], []]
+
+        def work(i):
+            for _ in range(30):
+                got[i].append(calls(i, streams[i]))
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert len(got[i]) == 30
+            for r in got[i]:
+                assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
