@@ -175,6 +175,27 @@ def test_a_smaller_batch_may_need_a_larger_workspace(tlc):
     assert torch.equal(y, (x.float() @ w[0].float().t()).bfloat16())
 
 
+@pytest.mark.parametrize("counts", [[70, 0, 130, 9], [2, 0, 5, 1]])
+def test_input_gradient_by_expert_from_columns_packed_one_by_one(tlc, counts):
+    """8 bits by expert: each expert's columns packed into its part of the codes, then one product of dy's rows."""
+    g = gen(16)
+    k, n, experts, rows = 300, 200, len(counts), sum(counts)
+    w, dy = randn(g, experts, n, k, scale=k ** -0.5).cuda(), randn(g, rows, n).cuda()
+    back = tlc.Rows8(torch.empty(experts * k, 256, dtype=torch.int8, device="cuda"),
+                     torch.empty(experts * k, device="cuda"), n)
+    for e in range(experts):
+        part = slice(e * k, (e + 1) * k)
+        tlc.q8_pack_columns(w[e], out=tlc.Rows8(back.codes[part], back.scales[part], n))
+    off = offsets_of(counts)
+    dx = tlc.q8_product(tlc.q8_pack_rows(dy), back, torch.float32, offsets=off.cuda())
+    for e, (b, t) in enumerate(ref.spans(off.tolist(), rows)):
+        (a, sa), (c, sc) = ref.pack_rows(dy[b:t].cpu()) if t > b else (None, None), ref.pack_columns(w[e].cpu())
+        if t > b:
+            want, _ = ref.product8(a, sa, c, sc)
+            # sums below 2^24 are exact, the products with the scales round
+            assert_close(dx[b:t], want, 3.01 * 2.0 ** -24 * want.abs(), e)
+
+
 # ---- codes and scales --------------------------------------------------------
 
 
