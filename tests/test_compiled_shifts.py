@@ -60,7 +60,7 @@ def test_the_rule_itself():
 def test_no_shift_by_a_waves_last_register(tmp_path):
     if not os.path.exists(os.path.join(LLVM, "llvm-objdump")):
         pytest.skip("LLVM's tools are not installed")
-    tlc.lib()  # builds it if there is none
+    tlc.lib()
     with open(build.LIB, "rb") as f:
         objects = list(code_objects(f.read()))
     assert len(objects) == len(build.SOURCES)
